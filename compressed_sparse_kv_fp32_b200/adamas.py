@@ -12,6 +12,7 @@ Method: ADAMAS long-context sparse attention article (lnwmold.com/news/826806),
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from typing import Optional, Tuple
@@ -33,12 +34,15 @@ SYMBOLS = (
     "adamas_decode_step_static", "adamas_decode_step_append", "adamas_decode_step_ex",
     "adamas_static_device_error", "adamas_debug_withhold_stage",
     "adamas_shard_workspace_bytes", "adamas_shard_score", "adamas_shard_attend", "adamas_merge_partials",
+    "adamas_rope_append", "adamas_chunk_workspace_bytes", "adamas_chunk_attend", "adamas_accumulate_chunk",
+    "adamas_accumulate_kept", "adamas_evict",
 )
 
 SELECT_PER_HEAD = 0
 SELECT_GROUP_SHARED = 1
 DEVERR_INTERNAL = 0x4
 DEVERR_TABLE = 0x8
+DEVERR_OFFSETS = 0x10
 
 
 class DecodeArgs(ctypes.Structure):
@@ -55,6 +59,46 @@ class DecodeArgs(ctypes.Structure):
         ("block_table", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
         ("max_pages", ctypes.c_int), ("n_sink", ctypes.c_int), ("n_recent", ctypes.c_int), ("policy", ctypes.c_int),
     ]
+
+
+_P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_PAGED = [("block_table", _P), ("n_pages", _I64), ("page_size", _I), ("max_pages", _I)]
+_WORKSPACE = [("workspace", _P), ("workspace_bytes", _SZ)]
+
+
+class RopeArgs(ctypes.Structure):
+    """Mirror of adamas_rope_args (include/adamas.h), field for field."""
+
+    _fields_ = [("q", _P), ("k", _P), ("v", _P), ("q_stride", _I64), ("k_stride", _I64), ("v_stride", _I64),
+                ("cu_new", _P), ("cache_lens", _P), ("positions", _P), ("freqs", _P), ("rot_dim", _I),
+                ("interleaved", _I), ("mscale", ctypes.c_double), ("T", _I), ("B", _I), ("Hq", _I), ("Hkv", _I),
+                ("Nmax", _I64), ("d", _I), ("q_out", _P), ("K", _P), ("V", _P), ("codes", _P),
+                *_PAGED, *_WORKSPACE]
+
+
+class ChunkArgs(ctypes.Structure):
+    """Mirror of adamas_chunk_args (include/adamas.h), field for field."""
+
+    _fields_ = [("q", _P), ("K", _P), ("V", _P), ("cu_q", _P), ("seq_lens", _P), ("T", _I), ("B", _I), ("Hq", _I),
+                ("Hkv", _I), ("Nmax", _I64), ("d", _I), ("out", _P), ("lse", _P), ("mass", _P),
+                *_PAGED, *_WORKSPACE]
+
+
+class KeptArgs(ctypes.Structure):
+    """Mirror of adamas_kept_args (include/adamas.h), field for field."""
+
+    _fields_ = [("q", _P), ("K", _P), ("idx", _P), ("seq_lens", _P), ("B", _I), ("Hq", _I), ("Hkv", _I),
+                ("Nmax", _I64), ("d", _I), ("budget", _I), ("policy", _I), ("mass", _P), *_PAGED, *_WORKSPACE]
+
+
+class EvictArgs(ctypes.Structure):
+    """Mirror of adamas_evict_args (include/adamas.h), field for field."""
+
+    _fields_ = [("K", _P), ("V", _P), ("codes", _P), ("mass", _P), ("seq_lens", _P), ("B", _I), ("Hkv", _I),
+                ("Nmax", _I64), ("d", _I), ("keep", _I), ("n_sink", _I), ("n_recent", _I), ("kept", _P),
+                ("new_lens", _P), *_PAGED, ("K_out", _P), ("V_out", _P), ("codes_out", _P), ("mass_out", _P),
+                ("Nmax_out", _I64), ("block_table_out", _P), ("n_pages_out", _I64), ("page_size_out", _I),
+                ("max_pages_out", _I), *_WORKSPACE]
 
 
 class AdamasError(RuntimeError):
@@ -108,6 +152,13 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
         l.adamas_shard_attend.restype = I
         l.adamas_merge_partials.argtypes = [P, I, I, I, P, P]
         l.adamas_merge_partials.restype = I
+        for name, args in (("rope_append", RopeArgs), ("chunk_attend", ChunkArgs), ("accumulate_chunk", ChunkArgs),
+                           ("accumulate_kept", KeptArgs), ("evict", EvictArgs)):
+            fn = getattr(l, "adamas_" + name)
+            fn.argtypes = [ctypes.POINTER(args), P]
+            fn.restype = I
+        l.adamas_chunk_workspace_bytes.argtypes = [I, I, I, I, I]
+        l.adamas_chunk_workspace_bytes.restype = SZ
         l.adamas_debug_withhold_stage.argtypes = [I]
         l.adamas_debug_withhold_stage.restype = None
         _lib = l
@@ -402,3 +453,300 @@ def merge_partials(partials: torch.Tensor, out: Optional[torch.Tensor] = None,
     _check(load().adamas_merge_partials(partials.data_ptr(), n, B, Hq, out.data_ptr(), _stream(stream)),
            "adamas_merge_partials")
     return out
+
+
+# ---------------------------------------------------------------- cache operators
+def chunk_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, d: int = HEAD_DIM) -> int:
+    n = load().adamas_chunk_workspace_bytes(T, B, Hq, Hkv, d)
+    if n == 0:
+        raise AdamasError(-2, "adamas_chunk_workspace_bytes")
+    return int(n)
+
+
+class ChunkWorkspace(Workspace):
+    """Device workspace of chunk_attend for up to T packed rows (the other cache
+    operators take it, or any other Workspace, as well), zero-filled on creation."""
+
+    def __init__(self, T: int, B: int, Hq: int, Hkv: int, device=None, stream: Optional[torch.cuda.Stream] = None):
+        self.nbytes = chunk_workspace_bytes(T, B, Hq, Hkv)
+        self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device if device is not None else "cuda")
+        self.reset(stream)
+
+
+def rope_frequencies(rot_dim: int = HEAD_DIM, base: float = 10000.0, *, scaling: Optional[str] = None,
+                     factor: float = 1.0, original_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     device=None) -> Tuple[torch.Tensor, float]:
+    """The frequency table of rope_append and its factor on cos and sin: (freqs int64
+    [rot_dim / 2], mscale).  Pair j turns by base^(-2j / rot_dim) per position.
+
+    scaling, for contexts `factor` times the trained length original_len:
+      None      as trained
+      "linear"  every frequency divided by factor (positions interpolated)
+      "ntk"     base * factor^(rot_dim / (rot_dim - 2)): the slowest pair is slowed by
+                factor, the fastest hardly
+      "yarn"    pairs that turn more than beta_fast times within original_len as
+                trained, those below beta_slow turns divided by factor, a linear ramp
+                over the pairs between; mscale = 0.1 ln(factor) + 1
+    Evaluated in 64 bits; the table holds each frequency as a fraction of a turn times
+    2^64, so that far positions lose nothing."""
+    if rot_dim % 2 or not 0 <= rot_dim <= HEAD_DIM:
+        raise ValueError("rot_dim must be even and at most 128")
+    if base <= 1.0 or factor < 1.0:
+        raise ValueError("base must be above 1 and factor at least 1")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    half, mscale = rot_dim // 2, 1.0
+    if scaling == "ntk":
+        if rot_dim <= 2:
+            raise ValueError("ntk scaling needs rot_dim above 2")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = [base ** (-2.0 * j / rot_dim) for j in range(half)]
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    if scaling == "yarn":
+        def pair_of(turns):  # the pair that turns this often within original_len
+            return rot_dim * math.log(original_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+        lo = max(0, math.floor(pair_of(beta_fast)))
+        hi = min(half - 1, math.ceil(pair_of(beta_slow)))
+        ramp = [min(1.0, max(0.0, (j - lo) / max(hi - lo, 1e-3))) for j in range(half)]
+        freq = [f * (1.0 - r) + f / factor * r for f, r in zip(freq, ramp)]
+        mscale = 0.1 * math.log(factor) + 1.0
+    turns = [round(f / (2.0 * math.pi) * 2.0 ** 64) for f in freq]
+    return torch.tensor(turns, dtype=torch.int64, device=device if device is not None else "cuda"), mscale
+
+
+def _on(device: torch.device, t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple):
+    """An argument of a cache operator: on `device`, dense, of this type and shape; its
+    address (None for None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device_of(t: torch.Tensor, name: str) -> torch.device:
+    """The device of a call: that of its first tensor, which must be the current one
+    (the launch goes to the current device's stream)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _cache_of(dev, K, V, codes, B, block_table, suffix=""):
+    """Geometry of a cache: (Hkv, Nmax, (K, V, codes) addresses, (table, n_pages, page_size, max_pages))."""
+    if not isinstance(K, torch.Tensor) or K.dim() != 4 or K.shape[3] != HEAD_DIM:
+        raise ValueError(f"K{suffix} must be [B, Hkv, Nmax, 128] or [n_pages, Hkv, page_size, 128]")
+    lead, Hkv, rows, d = K.shape
+    if block_table is None:
+        if lead != B:
+            raise ValueError(f"K{suffix} must hold {B} sequences, got {lead}")
+        Nmax, paged = rows, (None, 0, 0, 0)
+    else:
+        if block_table.dim() != 2:
+            raise ValueError(f"block_table{suffix} must be [B, max_pages]")
+        pages = block_table.shape[1]
+        paged = (_on(dev, block_table, "block_table" + suffix, torch.int32, (B, pages)), lead, rows, pages)
+        Nmax = pages * rows
+    ptrs = (_on(dev, K, "K" + suffix, torch.bfloat16, K.shape), _on(dev, V, "V" + suffix, torch.bfloat16, K.shape),
+            _on(dev, codes, "codes" + suffix, torch.uint8, (lead, Hkv, rows, d // 4)))
+    return Hkv, Nmax, ptrs, paged
+
+
+def _packed_rows(dev, x: Optional[torch.Tensor], name: str):
+    """A packed batch [T, heads, 128] whose rows may be spaced: (T, heads, stride, address)."""
+    if x is None:
+        return None, 0, 0, None
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
+    if x.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {x.device}")
+    if x.dim() != 3 or x.shape[2] != HEAD_DIM:
+        raise ValueError(f"{name} must be [T, heads, 128]")
+    T, H, d = x.shape
+    if T and (x.stride(2) != 1 or (H > 1 and x.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    stride = x.stride(0) if T > 1 else max(H * d, x.stride(0) // 8 * 8)
+    return T, H, stride, x.data_ptr()
+
+
+def rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],
+                cu_new: torch.Tensor, cache_lens: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
+                freqs: torch.Tensor, workspace: Workspace, *, positions: Optional[torch.Tensor] = None,
+                interleaved: bool = False, mscale: float = 1.0, codes: Optional[torch.Tensor] = None,
+                block_table: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """Rotary positions of new rows, and their append to the cache (adamas_rope_append).
+
+    q [T, Hq, 128], k and v [T, Hkv, 128] bf16, packed by cu_new int32 [B + 1]; rows
+    may be spaced (parts of one projection's output).  Token i of sequence b is
+    rotated by positions[row] (int32 [T]; default: its slot) and goes to slot
+    cache_lens[b] + i (int32 [B]).  freqs, mscale: rope_frequencies.  The first
+    2 * len(freqs) dimensions are rotated.  codes (uint8, optional) receives the rotated keys' codes.
+    K, V, codes are written in place; returns the rotated queries [T, Hq, 128] (out;
+    may be q itself), rows of no sequence left as they were (in a new tensor: 0)."""
+    dev = _device_of(K, "K")
+    if (k is None) != (v is None):
+        raise ValueError("k and v go together")
+    if q is None and k is None:
+        raise ValueError("neither q nor k, v given")
+    if not isinstance(cache_lens, torch.Tensor) or cache_lens.dim() != 1:
+        raise ValueError("cache_lens must be [B]")
+    B = cache_lens.shape[0]
+    Hkv, Nmax, ptrs, paged = _cache_of(dev, K, V, codes, B, block_table)
+    Tq, Hq, sq, pq = _packed_rows(dev, q, "q")
+    Tk, Hk, sk, pk = _packed_rows(dev, k, "k")
+    Tv, Hv, sv, pv = _packed_rows(dev, v, "v")
+    T = Tk if q is None else Tq
+    if k is not None and (Tk != T or Tv != T or Hk != Hkv or Hv != Hkv):
+        raise ValueError(f"k and v must be [{T}, {Hkv}, 128]")
+    if freqs.dim() != 1:
+        raise ValueError("freqs must be [rot_dim / 2]")
+    if q is None:
+        if out is not None:
+            raise ValueError("out without q")
+    elif out is None:
+        out = torch.zeros((T, Hq, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+    a = RopeArgs(pq, pk, pv, sq, sk, sv, _on(dev, cu_new, "cu_new", torch.int32, (B + 1,)),
+                 _on(dev, cache_lens, "cache_lens", torch.int32, (B,)),
+                 _on(dev, positions, "positions", torch.int32, (T,)),
+                 _on(dev, freqs, "freqs", torch.int64, freqs.shape), 2 * freqs.shape[0], int(interleaved), mscale,
+                 T, B, Hq or Hkv, Hkv, Nmax, HEAD_DIM, _on(dev, out, "out", torch.bfloat16, (T, Hq, HEAD_DIM)),
+                 *ptrs, *paged, workspace.buffer.data_ptr(), workspace.nbytes)
+    _check(load().adamas_rope_append(ctypes.byref(a), _stream(stream)), "adamas_rope_append")
+    return out
+
+
+def _chunk_args(dev, q, K, V, cu_q, seq_lens, block_table):
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, 128]")
+    if not isinstance(seq_lens, torch.Tensor) or seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be [B]")
+    T, Hq, _ = q.shape
+    B = seq_lens.shape[0]
+    Hkv, Nmax, (pk, pv, _), paged = _cache_of(dev, K, V, None, B, block_table)
+    head = (_on(dev, q, "q", torch.bfloat16, (T, Hq, HEAD_DIM)), pk, pv,
+            _on(dev, cu_q, "cu_q", torch.int32, (B + 1,)), _on(dev, seq_lens, "seq_lens", torch.int32, (B,)),
+            T, B, Hq, Hkv, Nmax, HEAD_DIM)
+    return head, paged
+
+
+def chunk_attend(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.Tensor, seq_lens: torch.Tensor,
+                 workspace: Workspace, *, block_table: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Causal attention of a chunk of new tokens over the cache (adamas_chunk_attend).
+
+    q [T, Hq, 128] bf16 packed by cu_q int32 [B + 1]; sequence b's rows are the last
+    ones of its seq_lens[b] cached tokens (K, V already appended).  Returns (out [T,
+    Hq, 128] bf16, lse [T, Hq] fp32, natural logarithm); rows of no sequence are left
+    as they were (in new tensors: 0).  workspace: ChunkWorkspace of at least T rows."""
+    dev = _device_of(q, "q")
+    head, paged = _chunk_args(dev, q, K, V, cu_q, seq_lens, block_table)
+    T, Hq = head[5], head[7]
+    if out is None:
+        out = torch.zeros((T, Hq, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.zeros((T, Hq), dtype=torch.float32, device=dev)
+    a = ChunkArgs(*head, _on(dev, out, "out", torch.bfloat16, (T, Hq, HEAD_DIM)),
+                  _on(dev, lse, "lse", torch.float32, (T, Hq)), None, *paged, workspace.buffer.data_ptr(),
+                  workspace.nbytes)
+    _check(load().adamas_chunk_attend(ctypes.byref(a), _stream(stream)), "adamas_chunk_attend")
+    return out, lse
+
+
+def accumulate_chunk(q: torch.Tensor, K: torch.Tensor, lse: torch.Tensor, cu_q: torch.Tensor, seq_lens: torch.Tensor,
+                     mass: torch.Tensor, workspace: Workspace, *, block_table: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Adds to mass [B, Hkv, Nmax] fp32 the attention weight each cached token received
+    from the chunk's rows (adamas_accumulate_chunk); q, cu_q, seq_lens and lse as of
+    chunk_attend (or its last rows alone).  Returns mass."""
+    dev = _device_of(q, "q")
+    head, paged = _chunk_args(dev, q, K, None, cu_q, seq_lens, block_table)
+    T, B, Hq, Hkv, Nmax = head[5:10]
+    a = ChunkArgs(*head, None, _on(dev, lse, "lse", torch.float32, (T, Hq)),
+                  _on(dev, mass, "mass", torch.float32, (B, Hkv, Nmax)), *paged, workspace.buffer.data_ptr(),
+                  workspace.nbytes)
+    _check(load().adamas_accumulate_chunk(ctypes.byref(a), _stream(stream)), "adamas_accumulate_chunk")
+    return mass
+
+
+def accumulate_kept(q: torch.Tensor, K: torch.Tensor, idx: torch.Tensor, seq_lens: torch.Tensor, mass: torch.Tensor,
+                    workspace: Workspace, *, policy: int = SELECT_PER_HEAD,
+                    block_table: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Adds to mass [B, Hkv, Nmax] fp32 the attention weights of a decode step's kept
+    tokens (adamas_accumulate_kept): q [B, Hq, 128] and idx as of decode_step / decode,
+    [B, Hq, budget] or, group-shared, [B, Hkv, budget].  Returns mass."""
+    dev = _device_of(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, 128]")
+    B, Hq, _ = q.shape
+    Hkv, Nmax, (pk, _, _), paged = _cache_of(dev, K, None, None, B, block_table)
+    if idx.dim() != 3:
+        raise ValueError("idx must be [B, Hq, budget] or, group-shared, [B, Hkv, budget]")
+    budget = idx.shape[2]
+    rows = Hkv if policy == SELECT_GROUP_SHARED else Hq
+    a = KeptArgs(_on(dev, q, "q", torch.bfloat16, (B, Hq, HEAD_DIM)), pk,
+                 _on(dev, idx, "idx", torch.int32, (B, rows, budget)),
+                 _on(dev, seq_lens, "seq_lens", torch.int32, (B,)), B, Hq, Hkv, Nmax, HEAD_DIM, budget, policy,
+                 _on(dev, mass, "mass", torch.float32, (B, Hkv, Nmax)), *paged, workspace.buffer.data_ptr(),
+                 workspace.nbytes)
+    _check(load().adamas_accumulate_kept(ctypes.byref(a), _stream(stream)), "adamas_accumulate_kept")
+    return mass
+
+
+def evict(K: torch.Tensor, V: torch.Tensor, mass: torch.Tensor, seq_lens: torch.Tensor, keep: int,
+          workspace: Workspace, *, codes: Optional[torch.Tensor] = None, n_sink: int = 0, n_recent: int = 0,
+          block_table: Optional[torch.Tensor] = None, K_out: Optional[torch.Tensor] = None,
+          V_out: Optional[torch.Tensor] = None, codes_out: Optional[torch.Tensor] = None,
+          mass_out: Optional[torch.Tensor] = None, table_out: Optional[torch.Tensor] = None,
+          kept: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+          stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Keeps the `keep` tokens of largest mass per (b, kv head), sinks and recent tokens
+    first, and moves their K, V, codes and mass to the front in their old order
+    (adamas_evict): in place, or into K_out, V_out, codes_out, mass_out (table_out:
+    their block table).  Returns (kept int32 [B, Hkv, keep]: the old slots, -1 past the
+    sequence's count; new_lens int32 [B])."""
+    dev = _device_of(K, "K")
+    if not isinstance(seq_lens, torch.Tensor) or seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be [B]")
+    B = seq_lens.shape[0]
+    Hkv, Nmax, ptrs, paged = _cache_of(dev, K, V, codes, B, block_table)
+    in_place = K_out is None
+    if in_place:
+        if V_out is not None or codes_out is not None or mass_out is not None or table_out is not None:
+            raise ValueError("V_out, codes_out, mass_out and table_out go with K_out")
+        ptrs_out, Nmax_out, paged_out = (None, None, None), 0, (None, 0, 0, 0)
+    else:
+        if V_out is None or mass_out is None or (codes is None) != (codes_out is None):
+            raise ValueError("K_out goes with V_out, mass_out and, when codes is given, codes_out")
+        Hkv_out, Nmax_out, ptrs_out, paged_out = _cache_of(dev, K_out, V_out, codes_out, B, table_out, "_out")
+        if Hkv_out != Hkv:
+            raise ValueError(f"K_out must have {Hkv} kv heads, got {Hkv_out}")
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=dev)
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    a = EvictArgs(*ptrs, _on(dev, mass, "mass", torch.float32, (B, Hkv, Nmax)),
+                  _on(dev, seq_lens, "seq_lens", torch.int32, (B,)), B, Hkv, Nmax, HEAD_DIM, keep, n_sink, n_recent,
+                  _on(dev, kept, "kept", torch.int32, (B, Hkv, max(keep, 0))),
+                  _on(dev, new_lens, "new_lens", torch.int32, (B,)), *paged, *ptrs_out,
+                  _on(dev, mass_out, "mass_out", torch.float32, (B, Hkv, Nmax_out)), Nmax_out, *paged_out,
+                  workspace.buffer.data_ptr(), workspace.nbytes)
+    _check(load().adamas_evict(ctypes.byref(a), _stream(stream)), "adamas_evict")
+    return kept, new_lens

@@ -2,8 +2,9 @@
 
     python -m compressed_sparse_kv_fp32_b200.build [--force] [-v]
 
-The library is csrc/adamas.cu (the C ABI, the key encoder, the distance dump)
-plus csrc/decode_inst.cu compiled once per query-head group size (1..8) so that
+The library is csrc/adamas.cu (the C ABI, the key encoder, the distance dump),
+csrc/cache_ops.cu (the cache operators: rotary append, chunk attention, accumulated
+attention weights, eviction) and csrc/decode_inst.cu compiled once per query-head group size (1..8) so that
 the decode kernel's instances compile in parallel; the objects are linked into
 libadamas.so next to this file.
 """
@@ -19,6 +20,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIBRARY = os.path.join(HERE, "libadamas.so")
 MAIN_SOURCE = os.path.join(HERE, "csrc", "adamas.cu")
+CACHE_OPS_SOURCE = os.path.join(HERE, "csrc", "cache_ops.cu")
 DECODE_SOURCE = os.path.join(HERE, "csrc", "decode_inst.cu")
 HEADER = os.path.join(ROOT, "include", "adamas.h")
 GROUP_SIZES = range(1, 9)
@@ -58,7 +60,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose else []
-    jobs = [[nvcc, *COMPILE_FLAGS, *extra, "-c", "-o", os.path.join(objdir, f"adamas{tag}.o"), MAIN_SOURCE]]
+    jobs = [[nvcc, *COMPILE_FLAGS, *extra, "-c", "-o", os.path.join(objdir, f"adamas{tag}.o"), MAIN_SOURCE],
+            [nvcc, *COMPILE_FLAGS, *extra, "-c", "-o", os.path.join(objdir, f"cache_ops{tag}.o"), CACHE_OPS_SOURCE]]
     for g in GROUP_SIZES:
         jobs.append([nvcc, *COMPILE_FLAGS, *extra, f"-DADAMAS_DECODE_G={g}", "-c",
                      "-o", os.path.join(objdir, f"decode_g{g}{tag}.o"), DECODE_SOURCE])

@@ -252,8 +252,9 @@ static std::mutex g_mutex;
 static DeviceInfo g_devices[kMaxDevices];
 static thread_local cudaError_t g_last_cuda_error = cudaSuccess;
 
-// Record a failed CUDA call for adamas_last_error_string and map it to a status.
-static int cuda_fail(cudaError_t e) {
+// Record a failed CUDA call for adamas_last_error_string and map it to a status
+// (also for the cache operators' translation unit).
+int cuda_fail(cudaError_t e) {
   g_last_cuda_error = e;
   return ADAMAS_ERR_CUDA;
 }

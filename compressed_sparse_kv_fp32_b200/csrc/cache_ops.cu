@@ -1,0 +1,260 @@
+// C ABI of the cache operators (declared in include/adamas.h): rotary append, chunk
+// attention, accumulated attention weights, eviction.  Argument checks and launches.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/adamas.h"
+#include "chunk.cuh"
+#include "evict.cuh"
+#include "rope.cuh"
+
+namespace adamas {
+
+int cuda_fail(cudaError_t e);  // adamas.cu: records the error, returns ADAMAS_ERR_CUDA
+
+static_assert(kErrOffsets == ADAMAS_DEVERR_OFFSETS, "error bits of the header");
+
+constexpr size_t kCtrlBytes = 256;  // control words at the start of every workspace
+
+static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// Sizes common to the operators (Hq = Hkv where a call has no query heads).
+static int check_heads(int B, int Hq, int Hkv, int d) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return ADAMAS_ERR_INVALID_ARG;
+  if (d != kDim) return ADAMAS_ERR_UNSUPPORTED;
+  if (Hq / Hkv > kMaxGroup || B > kMaxBatch || (int64_t)B * Hkv > 65535) return ADAMAS_ERR_UNSUPPORTED;
+  return ADAMAS_OK;
+}
+
+static int make_geom(const int32_t* table, int64_t n_pages, int page_size, int max_pages, int64_t Nmax, int Hkv,
+                     CacheGeom* g) {
+  g->table = table;
+  g->Hkv = Hkv;
+  g->Nmax = Nmax;
+  g->n_pages = 0;
+  g->max_pages = 0;
+  if (table) {
+    if (page_size < 1 || max_pages < 1 || n_pages < 1 || !aligned(table, 4)) return ADAMAS_ERR_INVALID_ARG;
+    g->Nmax = (int64_t)max_pages * page_size;
+    g->n_pages = n_pages;
+    g->max_pages = max_pages;
+    g->page = FastDiv::of((uint32_t)page_size);
+  }
+  if (g->Nmax < 0) return ADAMAS_ERR_INVALID_ARG;
+  if (g->Nmax > INT32_MAX) return ADAMAS_ERR_UNSUPPORTED;
+  return ADAMAS_OK;
+}
+
+static int check_ctrl(const void* ws, size_t bytes, size_t need) {
+  return !ws || bytes < need || !aligned(ws, 16) ? ADAMAS_ERR_WORKSPACE : ADAMAS_OK;
+}
+
+static uint32_t* err_word(void* ws) { return static_cast<uint32_t*>(ws) + 2; }
+
+static int launched() {
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? cuda_fail(e) : ADAMAS_OK;
+}
+
+static int fill_chunk(const adamas_chunk_args& a, bool attend, ChunkParams* p) {
+  int rc = check_heads(a.B, a.Hq, a.Hkv, a.d);
+  if (rc != ADAMAS_OK) return rc;
+  if (a.T < 0) return ADAMAS_ERR_INVALID_ARG;
+  if ((rc = make_geom(a.block_table, a.n_pages, a.page_size, a.max_pages, a.Nmax, a.Hkv, &p->geo)) != ADAMAS_OK)
+    return rc;
+  if (a.B == 0 || a.T == 0) return ADAMAS_OK;
+  if (!a.q || !a.cu_q || !a.seq_lens || (p->geo.Nmax > 0 && (!a.K || (attend && !a.V)))) return ADAMAS_ERR_INVALID_ARG;
+  if (attend ? !a.out : (!a.lse || (p->geo.Nmax > 0 && !a.mass))) return ADAMAS_ERR_INVALID_ARG;
+  if (!aligned(a.q, 16) || !aligned(a.K, 16) || !aligned(a.V, 16) || !aligned(a.out, 16) || !aligned(a.lse, 4) ||
+      !aligned(a.mass, 4) || !aligned(a.cu_q, 4) || !aligned(a.seq_lens, 4))
+    return ADAMAS_ERR_INVALID_ARG;
+  p->q = static_cast<const uint16_t*>(a.q);
+  p->K = static_cast<const uint16_t*>(a.K);
+  p->V = static_cast<const uint16_t*>(a.V);
+  p->cu_q = a.cu_q;
+  p->seq_lens = a.seq_lens;
+  p->T = a.T;
+  p->B = a.B;
+  p->Hq = a.Hq;
+  p->Hkv = a.Hkv;
+  p->G = a.Hq / a.Hkv;
+  p->out = static_cast<uint16_t*>(a.out);
+  p->lse = a.lse;
+  p->mass = a.mass;
+  return ADAMAS_OK;
+}
+
+}  // namespace adamas
+
+using namespace adamas;
+
+extern "C" {
+
+int adamas_rope_append(const adamas_rope_args* args, adamas_stream_t stream) {
+  if (!args) return ADAMAS_ERR_INVALID_ARG;
+  const adamas_rope_args& a = *args;
+  int rc = check_heads(a.B, a.Hq, a.Hkv, a.d);
+  if (rc != ADAMAS_OK) return rc;
+  if (a.T < 0 || a.rot_dim < 0 || a.rot_dim > kDim || a.rot_dim % 2 != 0) return ADAMAS_ERR_INVALID_ARG;
+  RopeParams p = {};
+  if ((rc = make_geom(a.block_table, a.n_pages, a.page_size, a.max_pages, a.Nmax, a.Hkv, &p.geo)) != ADAMAS_OK)
+    return rc;
+  if ((a.k == nullptr) != (a.v == nullptr)) return ADAMAS_ERR_INVALID_ARG;
+  if (a.B == 0 || a.T == 0 || (!a.q && !a.k)) return ADAMAS_OK;
+  if (!a.cu_new || !a.cache_lens || (a.rot_dim > 0 && !a.freqs)) return ADAMAS_ERR_INVALID_ARG;
+  if (a.q && (!a.q_out || !aligned(a.q, 16) || !aligned(a.q_out, 16) || a.q_stride < (int64_t)a.Hq * kDim ||
+              a.q_stride % 8 != 0 || (a.q_out == a.q && a.q_stride != (int64_t)a.Hq * kDim)))
+    return ADAMAS_ERR_INVALID_ARG;
+  if (a.k && ((p.geo.Nmax > 0 && (!a.K || !a.V)) || !aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.K, 16) ||
+              !aligned(a.V, 16) || !aligned(a.codes, 32) || a.k_stride < (int64_t)a.Hkv * kDim ||
+              a.v_stride < (int64_t)a.Hkv * kDim || a.k_stride % 8 != 0 || a.v_stride % 8 != 0))
+    return ADAMAS_ERR_INVALID_ARG;
+  if (!aligned(a.cu_new, 4) || !aligned(a.cache_lens, 4) || !aligned(a.positions, 4) || !aligned(a.freqs, 8))
+    return ADAMAS_ERR_INVALID_ARG;
+  if ((rc = check_ctrl(a.workspace, a.workspace_bytes, kCtrlBytes)) != ADAMAS_OK) return rc;
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.k = static_cast<const uint16_t*>(a.k);
+  p.v = static_cast<const uint16_t*>(a.v);
+  p.q_stride = a.q_stride;
+  p.k_stride = a.k_stride;
+  p.v_stride = a.v_stride;
+  p.cu_new = a.cu_new;
+  p.cache_lens = a.cache_lens;
+  p.positions = a.positions;
+  p.freqs = a.freqs;
+  p.rot = a.rot_dim;
+  p.interleaved = a.interleaved != 0;
+  p.mscale = a.mscale;
+  p.T = a.T;
+  p.B = a.B;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.q_out = static_cast<uint16_t*>(a.q_out);
+  p.K = static_cast<uint16_t*>(a.K);
+  p.V = static_cast<uint16_t*>(a.V);
+  p.codes = a.codes;
+  p.err = err_word(a.workspace);
+  rope_append_kernel<<<dim3((unsigned)a.T, 1), kRopeThreads, 0, (cudaStream_t)stream>>>(p);
+  return launched();
+}
+
+size_t adamas_chunk_workspace_bytes(int T, int B, int Hq, int Hkv, int d) {
+  if (T < 0 || check_heads(B, Hq, Hkv, d) != ADAMAS_OK) return 0;
+  return kCtrlBytes;
+}
+
+int adamas_chunk_attend(const adamas_chunk_args* args, adamas_stream_t stream) {
+  if (!args) return ADAMAS_ERR_INVALID_ARG;
+  const adamas_chunk_args& a = *args;
+  ChunkParams p = {};
+  int rc = fill_chunk(a, true, &p);
+  if (rc != ADAMAS_OK || a.B == 0 || a.T == 0) return rc;
+  if ((rc = check_ctrl(a.workspace, a.workspace_bytes, adamas_chunk_workspace_bytes(a.T, a.B, a.Hq, a.Hkv, a.d))) !=
+      ADAMAS_OK)
+    return rc;
+  p.err = err_word(a.workspace);
+  const int64_t items = (int64_t)a.T * a.Hq;
+  chunk_attend_rows_kernel<<<(unsigned)((items + 3) / 4), 128, 0, (cudaStream_t)stream>>>(p);
+  return launched();
+}
+
+int adamas_accumulate_chunk(const adamas_chunk_args* args, adamas_stream_t stream) {
+  if (!args) return ADAMAS_ERR_INVALID_ARG;
+  const adamas_chunk_args& a = *args;
+  ChunkParams p = {};
+  int rc = fill_chunk(a, false, &p);
+  if (rc != ADAMAS_OK || a.B == 0 || a.T == 0 || p.geo.Nmax == 0) return rc;
+  if ((rc = check_ctrl(a.workspace, a.workspace_bytes, kCtrlBytes)) != ADAMAS_OK) return rc;
+  p.err = err_word(a.workspace);
+  const dim3 grid((unsigned)((p.geo.Nmax + 127) / 128), (unsigned)(a.B * a.Hkv));
+  accumulate_chunk_rows_kernel<<<grid, 128, 0, (cudaStream_t)stream>>>(p);
+  return launched();
+}
+
+int adamas_accumulate_kept(const adamas_kept_args* args, adamas_stream_t stream) {
+  if (!args) return ADAMAS_ERR_INVALID_ARG;
+  const adamas_kept_args& a = *args;
+  int rc = check_heads(a.B, a.Hq, a.Hkv, a.d);
+  if (rc != ADAMAS_OK) return rc;
+  if (a.budget < 0 || (a.policy != ADAMAS_SELECT_PER_HEAD && a.policy != ADAMAS_SELECT_GROUP_SHARED))
+    return ADAMAS_ERR_INVALID_ARG;
+  KeptParams p = {};
+  if ((rc = make_geom(a.block_table, a.n_pages, a.page_size, a.max_pages, a.Nmax, a.Hkv, &p.geo)) != ADAMAS_OK)
+    return rc;
+  if (a.B == 0 || a.budget == 0 || p.geo.Nmax == 0) return ADAMAS_OK;
+  if (!a.q || !a.K || !a.idx || !a.seq_lens || !a.mass) return ADAMAS_ERR_INVALID_ARG;
+  if (!aligned(a.q, 16) || !aligned(a.K, 16) || !aligned(a.idx, 4) || !aligned(a.seq_lens, 4) || !aligned(a.mass, 4))
+    return ADAMAS_ERR_INVALID_ARG;
+  if ((rc = check_ctrl(a.workspace, a.workspace_bytes, kCtrlBytes)) != ADAMAS_OK) return rc;
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.K = static_cast<const uint16_t*>(a.K);
+  p.idx = a.idx;
+  p.seq_lens = a.seq_lens;
+  p.B = a.B;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.G = a.Hq / a.Hkv;
+  p.budget = a.budget;
+  p.shared_rows = a.policy == ADAMAS_SELECT_GROUP_SHARED;
+  p.mass = a.mass;
+  p.err = err_word(a.workspace);
+  accumulate_kept_kernel<<<(unsigned)(a.B * a.Hkv), 256, 0, (cudaStream_t)stream>>>(p);
+  return launched();
+}
+
+int adamas_evict(const adamas_evict_args* args, adamas_stream_t stream) {
+  if (!args) return ADAMAS_ERR_INVALID_ARG;
+  const adamas_evict_args& a = *args;
+  int rc = check_heads(a.B, a.Hkv, a.Hkv, a.d);
+  if (rc != ADAMAS_OK) return rc;
+  if (a.keep < 0 || a.n_sink < 0 || a.n_recent < 0) return ADAMAS_ERR_INVALID_ARG;
+  EvictParams p = {};
+  if ((rc = make_geom(a.block_table, a.n_pages, a.page_size, a.max_pages, a.Nmax, a.Hkv, &p.geo)) != ADAMAS_OK)
+    return rc;
+  const bool in_place = !a.K_out && !a.V_out && !a.codes_out && !a.mass_out && !a.block_table_out;
+  if (in_place) {
+    p.out = p.geo;
+  } else {
+    if ((rc = make_geom(a.block_table_out, a.n_pages_out, a.page_size_out, a.max_pages_out, a.Nmax_out, a.Hkv,
+                        &p.out)) != ADAMAS_OK)
+      return rc;
+    if (p.out.Nmax < a.keep) return ADAMAS_ERR_INVALID_ARG;
+    if ((a.codes == nullptr) != (a.codes_out == nullptr)) return ADAMAS_ERR_INVALID_ARG;
+  }
+  if (a.B == 0 || (p.geo.Nmax == 0 && p.out.Nmax == 0)) return ADAMAS_OK;
+  if (!a.seq_lens || !a.new_lens || a.new_lens == a.seq_lens || (a.keep > 0 && !a.kept)) return ADAMAS_ERR_INVALID_ARG;
+  if (p.geo.Nmax > 0 && (!a.K || !a.V || !a.mass)) return ADAMAS_ERR_INVALID_ARG;
+  if (!in_place && ((a.keep > 0 && (!a.K_out || !a.V_out)) || !a.mass_out || a.K_out == a.K || a.V_out == a.V ||
+                    a.mass_out == a.mass || (a.codes && a.codes_out == a.codes)))
+    return ADAMAS_ERR_INVALID_ARG;
+  if (!aligned(a.K, 16) || !aligned(a.V, 16) || !aligned(a.codes, 32) || !aligned(a.mass, 4) || !aligned(a.K_out, 16) ||
+      !aligned(a.V_out, 16) || !aligned(a.codes_out, 32) || !aligned(a.mass_out, 4) || !aligned(a.kept, 4) ||
+      !aligned(a.seq_lens, 4) || !aligned(a.new_lens, 4))
+    return ADAMAS_ERR_INVALID_ARG;
+  if ((rc = check_ctrl(a.workspace, a.workspace_bytes, kCtrlBytes)) != ADAMAS_OK) return rc;
+  p.K = static_cast<const uint16_t*>(a.K);
+  p.V = static_cast<const uint16_t*>(a.V);
+  p.codes = a.codes;
+  p.mass = a.mass;
+  p.seq_lens = a.seq_lens;
+  p.B = a.B;
+  p.Hkv = a.Hkv;
+  p.keep = a.keep;
+  p.n_sink = a.n_sink;
+  p.n_recent = a.n_recent;
+  p.kept = a.kept;
+  p.new_lens = a.new_lens;
+  p.K_out = static_cast<uint16_t*>(in_place ? a.K : a.K_out);
+  p.V_out = static_cast<uint16_t*>(in_place ? a.V : a.V_out);
+  p.codes_out = in_place ? a.codes : a.codes_out;
+  p.mass_out = in_place ? a.mass : a.mass_out;
+  p.err = err_word(a.workspace);
+  const unsigned grid = (unsigned)(a.B * a.Hkv);
+  evict_select_kernel<<<grid, kSelThreads, 0, (cudaStream_t)stream>>>(p);
+  evict_move_kernel<<<grid, kMoveThreads, 0, (cudaStream_t)stream>>>(p);
+  return launched();
+}
+
+}  // extern "C"

@@ -65,7 +65,9 @@ enum adamas_status {
 #define ADAMAS_DEVERR_SEQLEN 0x1u  /* a seq_lens entry was outside [0, Nmax]; it was clamped */
 #define ADAMAS_DEVERR_TIMEOUT 0x2u /* a bounded wait on a stage copy gave up; the step's outputs are invalid */
 #define ADAMAS_DEVERR_INTERNAL 0x4u /* a block's share exceeded its planned size; outputs are invalid */
-#define ADAMAS_DEVERR_TABLE 0x8u    /* a block-table entry was outside [0, n_pages); page 0 was read instead */
+#define ADAMAS_DEVERR_TABLE 0x8u    /* a block-table entry was outside [0, n_pages); page 0 was read instead
+                                       (calls that write through the table write nothing there) */
+#define ADAMAS_DEVERR_OFFSETS 0x10u /* offsets of a ragged batch were not ascending within [0, T] */
 
 /* Selection policies of adamas_decode_step_ex. */
 enum adamas_select_policy {
@@ -352,6 +354,215 @@ int adamas_shard_attend(const void *q, const void *K, const void *V, const int32
  * are skipped; 0 when every state is empty).  16-byte aligned fp32 arrays.
  */
 int adamas_merge_partials(const float *partials, int n, int B, int Hq, float *out, adamas_stream_t stream);
+
+/* ======================================================================== cache operators
+ * What a serving loop runs around the decode step, over the same cache: rotary
+ * positions and the append of new rows, attention of a chunk of new tokens, the
+ * attention weight that each cached token has received, and the eviction of the
+ * tokens that received least.
+ *
+ * Shared conventions (besides the ones at the top of this file)
+ *   - A cache is contiguous, K and V [B][Hkv][Nmax][128], or paged (block_table
+ *     given): [n_pages][Hkv][page_size][128] read through block_table
+ *     [B][max_pages], with Nmax ignored and max_pages * page_size tokens per
+ *     sequence, exactly as in adamas_decode_args.  codes follow with 32 B rows.
+ *     Token numbers below ("slots") are positions in the sequence's cache.
+ *   - A ragged batch of new tokens is packed: sequence b owns rows
+ *     [cu[b], cu[b + 1]) of the T rows, cu device int32 [B + 1], ascending within
+ *     [0, T] (else ADAMAS_DEVERR_OFFSETS, and the sequence is left out).  Rows
+ *     before cu[0] and from cu[B] on belong to no sequence: nothing is read from
+ *     them and their outputs are left as they were.
+ *   - mass device fp32 [B][Hkv][Nmax] (paged: Nmax = max_pages * page_size, by slot
+ *     and not by page): the attention weight a token received so far, summed over
+ *     query rows and over the query heads of its kv head.
+ *   - workspace: adamas_chunk_workspace_bytes for adamas_chunk_attend; for the other
+ *     calls any workspace of this library (the device error word in its first 256
+ *     bytes is all they use).  Zero-filled once (adamas_workspace_init).
+ *   - Slots at or past a sequence's length may hold anything, NaN included; rows
+ *     inside it must be finite.
+ */
+
+/*
+ * Rotary positions of new query and key rows, and the append of the new rows to
+ * the cache.  Token i of sequence b (row r = cu_new[b] + i) is rotated by its
+ * position p = positions[r] (or its slot when positions is NULL) and goes to slot
+ * cache_lens[b] + i; a slot outside [0, Nmax) is not written.
+ *   pair j of the rotated part (the first rot_dim dimensions; the rest pass
+ *   unchanged): dimensions (j, j + rot_dim / 2), or (2j, 2j + 1) when interleaved;
+ *   turn = freqs[j] * p mod 2^64, in 2^-64 turns (so p may be any int32, and the
+ *   angle of a far position is as exact as that of a near one);
+ *   c = RN32(mscale cos), s = RN32(mscale sin) of that angle, evaluated in 64 bits;
+ *   (x1, x2) -> (RN32(x1 c) - RN32(x2 s), RN32(x2 c) + RN32(x1 s)), each rounded to
+ *   fp32 and then once to bf16: the same bits on every run and batch shape, so that
+ *   the codes made from them are reproducible too.
+ * codes (optional) receives the packed codes of the rotated keys, as
+ * adamas_encode_keys makes them.
+ *   q, k, v    device bf16, row r at q + r * q_stride (elements, a multiple of 8;
+ *              Hq or Hkv heads of 128 contiguous), so they may be parts of one
+ *              projection's output.  q may be NULL (nothing rotated), k and v both
+ *              NULL (nothing appended).
+ *   q_out      device bf16 [T][Hq][128]; may be q itself when q_stride = Hq * 128.
+ *   freqs      device uint64 [rot_dim / 2]: angle per position of each pair as a
+ *              fraction of a turn, times 2^64 (scaling methods change this table and mscale)
+ *   rot_dim    even, 0..128
+ * The slots written in one call must be distinct.
+ */
+typedef struct adamas_rope_args {
+    const void *q;
+    const void *k;
+    const void *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *cu_new;
+    const int32_t *cache_lens;
+    const int32_t *positions;
+    const uint64_t *freqs;
+    int rot_dim;
+    int interleaved;
+    double mscale;
+    int T, B, Hq, Hkv;
+    int64_t Nmax;
+    int d;
+    void *q_out;
+    void *K;
+    void *V;
+    uint8_t *codes;
+    const int32_t *block_table;
+    int64_t n_pages;
+    int page_size;
+    int max_pages;
+    void *workspace;
+    size_t workspace_bytes;
+} adamas_rope_args;
+
+int adamas_rope_append(const adamas_rope_args *args, adamas_stream_t stream);
+
+/*
+ * Causal attention of a chunk of new tokens over the whole cache (the new tokens'
+ * rows are already in it).  Sequence b has n_b = cu_q[b + 1] - cu_q[b] new tokens,
+ * the last n_b of its seq_lens[b] cached ones: query row i sits at slot
+ * seq_lens[b] - n_b + i and sees slots 0 .. that one, softmax scale 1/sqrt(128).
+ * n_b may be anything from 0 (the sequence is left out) over 1 (dense decode) to
+ * the whole prompt.  A row whose slot is negative sees nothing: out 0, lse -inf.
+ *   q    device bf16 [T][Hq][128]
+ *   out  device bf16 [T][Hq][128]
+ *   lse  device fp32 [T][Hq], optional: the natural logarithm of the row's sum of
+ *        exp(score)
+ * Scores, softmax statistics and output sums are fp32; the probabilities are
+ * rounded to bf16 for their product with V (V is bf16 as well), the sum they are
+ * divided by is not.  V rows are finite: a tile's masked products are 0 * V.
+ * The same inputs give the same bits on every run.
+ */
+typedef struct adamas_chunk_args {
+    const void *q;
+    const void *K;
+    const void *V;
+    const int32_t *cu_q;
+    const int32_t *seq_lens;
+    int T, B, Hq, Hkv;
+    int64_t Nmax;
+    int d;
+    void *out;
+    float *lse;
+    float *mass;
+    const int32_t *block_table;
+    int64_t n_pages;
+    int page_size;
+    int max_pages;
+    void *workspace;
+    size_t workspace_bytes;
+} adamas_chunk_args;
+
+/* Bytes of device workspace adamas_chunk_attend needs (0: unsupported sizes). */
+size_t adamas_chunk_workspace_bytes(int T, int B, int Hq, int Hkv, int d);
+
+/* Uses every field but mass. */
+int adamas_chunk_attend(const adamas_chunk_args *args, adamas_stream_t stream);
+
+/*
+ * mass[b][kvh][t] += sum over the chunk's rows that see slot t, and over the query
+ * heads of kvh, of exp(q.K_t / sqrt(128) - lse[row]): the weight that slot t had in
+ * the attention adamas_chunk_attend computed (lse as it wrote it).  To weigh the
+ * tokens by a prompt's last rows only, pass those rows as the chunk.  Rows with
+ * lse = -inf add nothing.  V and out are not used.
+ */
+int adamas_accumulate_chunk(const adamas_chunk_args *args, adamas_stream_t stream);
+
+/*
+ * The decode step's form: for every (b, query head) the softmax weights over the
+ * kept tokens idx lists (as adamas_decode_step wrote them; entries outside
+ * [0, seq_lens[b]) are skipped) are added to mass[b][kvh][idx].  idx is
+ * [B][Hq][budget], or [B][Hkv][budget] with policy ADAMAS_SELECT_GROUP_SHARED (one
+ * list for the query heads of a kv head).  Each list's tokens are distinct.
+ */
+typedef struct adamas_kept_args {
+    const void *q;
+    const void *K;
+    const int32_t *idx;
+    const int32_t *seq_lens;
+    int B, Hq, Hkv;
+    int64_t Nmax;
+    int d;
+    int budget;
+    int policy;
+    float *mass;
+    const int32_t *block_table;
+    int64_t n_pages;
+    int page_size;
+    int max_pages;
+    void *workspace;
+    size_t workspace_bytes;
+} adamas_kept_args;
+
+int adamas_accumulate_kept(const adamas_kept_args *args, adamas_stream_t stream);
+
+/*
+ * Eviction by accumulated attention weight.  For every (b, kv head) the
+ * k_b = min(keep, seq_lens[b]) tokens of largest mass are kept -- equal masses: the
+ * lower slot; -0 counts as 0, NaN as less than everything -- with the first n_sink
+ * and the last n_recent tokens ranked ahead of all others (in slot order).  The kept
+ * tokens move to slots 0 .. k_b - 1 in their old order: K, V, codes (optional) and
+ * mass; mass from slot k_b on is set to 0 (a token appended there starts with no
+ * weight).
+ *   kept      device int32 [B][Hkv][keep]: their old slots, ascending, -1 past k_b
+ *   new_lens  device int32 [B]: k_b; not seq_lens itself
+ *   K_out ... mass_out, block_table_out, n_pages_out, page_size_out, max_pages_out,
+ *             Nmax_out: the cache they move to, contiguous or paged; it must hold
+ *             keep tokens per sequence and share no memory with the source (the
+ *             rows of K_out past k_b are left as they were).  All NULL: in place, and no
+ *             page may then be shared between sequences.
+ */
+typedef struct adamas_evict_args {
+    void *K;
+    void *V;
+    uint8_t *codes;
+    float *mass;
+    const int32_t *seq_lens;
+    int B, Hkv;
+    int64_t Nmax;
+    int d;
+    int keep;
+    int n_sink;
+    int n_recent;
+    int32_t *kept;
+    int32_t *new_lens;
+    const int32_t *block_table;
+    int64_t n_pages;
+    int page_size;
+    int max_pages;
+    void *K_out;
+    void *V_out;
+    uint8_t *codes_out;
+    float *mass_out;
+    int64_t Nmax_out;
+    const int32_t *block_table_out;
+    int64_t n_pages_out;
+    int page_size_out;
+    int max_pages_out;
+    void *workspace;
+    size_t workspace_bytes;
+} adamas_evict_args;
+
+int adamas_evict(const adamas_evict_args *args, adamas_stream_t stream);
 
 /*
  * Synchronise `stream`, then copy the workspace's device error word into
