@@ -44,6 +44,18 @@ struct CacheGeom {
     phys = out ? 0 : phys;
     return (phys * Hkv + h) * page.d + slot;
   }
+  // The same in 32 bits, for caches of rows that real memory holds (2^32 rows are a
+  // terabyte).
+  __device__ __forceinline__ uint32_t row32(int b, int h, int t, bool& bad) const {
+    if (table == nullptr) return (uint32_t)(b * Hkv + h) * (uint32_t)Nmax + (uint32_t)t;
+    const uint32_t pg = page.div((uint32_t)t);
+    const uint32_t slot = (uint32_t)t - pg * page.d;
+    uint32_t phys = (uint32_t)table[(int64_t)b * max_pages + pg];
+    const bool out = phys >= (uint64_t)n_pages;  // a negative entry is a large one
+    bad |= out;
+    phys = out ? 0u : phys;
+    return (phys * (uint32_t)Hkv + (uint32_t)h) * page.d + slot;
+  }
 };
 
 __device__ __forceinline__ int64_t clamp_len(int64_t len, int64_t Nmax, bool& bad) {

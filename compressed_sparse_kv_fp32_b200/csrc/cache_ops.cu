@@ -2,11 +2,11 @@
 // attention, accumulated attention weights, eviction.  Argument checks and launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
-#include <cstring>
 
 #include "../../include/adamas.h"
-#include "chunk.cuh"
+#include "chunk_attend.cuh"
 #include "evict.cuh"
 #include "rope.cuh"
 
@@ -57,6 +57,35 @@ static int launched() {
   const cudaError_t e = cudaGetLastError();
   return e != cudaSuccess ? cuda_fail(e) : ADAMAS_OK;
 }
+
+// Multiprocessors of the current device, with the one-time set-up of chunk attention's
+// kernel on it: its shared memory, and the register count its split is made for.
+static int attend_device(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= 64) return ADAMAS_ERR_UNSUPPORTED;
+  if ((*sms = known[dev].load(std::memory_order_acquire)) > 0) return ADAMAS_OK;
+  const void* fn = reinterpret_cast<const void*>(&chunk_attend_kernel);
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, fn)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAtSmem)) != cudaSuccess ||
+      (e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return cuda_fail(e);
+  if (fa.numRegs != 65536 / kAtThreads) return ADAMAS_ERR_UNSUPPORTED;  // the warps' shares add up to 65536
+  if (*sms > kAtMaxGrid) *sms = kAtMaxGrid;
+  known[dev].store(*sms, std::memory_order_release);
+  return ADAMAS_OK;
+}
+
+// Workspace of chunk attention: control words | arrival counters | partial states.
+static int part_rows(int T, int G) {
+  const int tu = 2 * (128 / G);
+  return (T < tu ? T : tu) * G;
+}
+constexpr size_t kAtArrivedBytes = 1024;
+static_assert(kAtMaxGrid * sizeof(uint32_t) <= kAtArrivedBytes, "a counter per block");
 
 static int fill_chunk(const adamas_chunk_args& a, bool attend, ChunkParams* p) {
   int rc = check_heads(a.B, a.Hq, a.Hkv, a.d);
@@ -142,7 +171,7 @@ int adamas_rope_append(const adamas_rope_args* args, adamas_stream_t stream) {
 
 size_t adamas_chunk_workspace_bytes(int T, int B, int Hq, int Hkv, int d) {
   if (T < 0 || check_heads(B, Hq, Hkv, d) != ADAMAS_OK) return 0;
-  return kCtrlBytes;
+  return kCtrlBytes + kAtArrivedBytes + (size_t)2 * kAtMaxGrid * part_rows(T, Hq / Hkv) * kAtPartRow * sizeof(float);
 }
 
 int adamas_chunk_attend(const adamas_chunk_args* args, adamas_stream_t stream) {
@@ -155,8 +184,19 @@ int adamas_chunk_attend(const adamas_chunk_args* args, adamas_stream_t stream) {
       ADAMAS_OK)
     return rc;
   p.err = err_word(a.workspace);
-  const int64_t items = (int64_t)a.T * a.Hq;
-  chunk_attend_rows_kernel<<<(unsigned)((items + 3) / 4), 128, 0, (cudaStream_t)stream>>>(p);
+  int sms = 0;
+  if ((rc = attend_device(&sms)) != ADAMAS_OK) return rc;
+  unsigned char* ws = static_cast<unsigned char*>(a.workspace);
+  AtParams ap;
+  ap.c = p;
+  ap.arrived = reinterpret_cast<uint32_t*>(ws + kCtrlBytes);
+  ap.part = reinterpret_cast<float*>(ws + kCtrlBytes + kAtArrivedBytes);
+  ap.part_rows = part_rows(a.T, p.G);
+  ap.TQ = 128 / p.G;
+  // no more blocks than K/V tiles of all units
+  const int64_t units = (int64_t)p.Hkv * ((a.T + 2 * ap.TQ - 1) / (2 * ap.TQ) + p.B);
+  const int64_t tiles = units * ((p.geo.Nmax + 127) / 128 + 1);
+  chunk_attend_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kAtThreads, kAtSmem, (cudaStream_t)stream>>>(ap);
   return launched();
 }
 

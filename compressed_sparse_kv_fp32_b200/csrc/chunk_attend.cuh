@@ -1,0 +1,593 @@
+// Causal attention of a ragged chunk of new tokens over the cache, on the tensor
+// cores: one persistent kernel for one new token per sequence as for whole prompts.
+//
+// A unit is the work of one (sequence, kv head) and up to 2 x floor(128 / G) new
+// tokens: their G query heads are the rows of two 128-row tiles, which share every
+// K and V tile of 128 tokens.  Per tile: S = Q K^T (fp32, tensor memory), one running
+// maximum and sum per row, P = exp2(s c - m) rounded to bf16 in tensor memory over S,
+// O += P V (fp32, tensor memory).  The maximum that scales a row is raised only when a
+// score exceeds it by more than 2^8 in the exponent, so O is hardly ever rescaled; the
+// quotient is the same for every choice of it, and P and the sum stay far from fp32's
+// and bf16's range.
+//
+// Roles: warps 0-3 and 4-7 one row per thread of tile 0 and 1 (softmax, rescaling,
+// epilogue); warps 8-11 copy Q, K and V rows through the block table with cp.async
+// (any page size, tails filled with zeros); one thread of warp 12 issues the products.
+// While one tile's softmax runs, the other tile's products do.
+//
+// Work split.  Sequences with several units (prompts) fill whole waves of the grid,
+// heads that fit in L2 together next to each other and the longest units first, so that
+// the blocks of a wave read the same K and V tiles at about the same time.  What is left
+// over, and every sequence with a single unit (decode), is one line of K/V tiles cut
+// into equal shares, one per block: a unit cut by a share's end leaves partial states
+// in the workspace, and the block that arrives last merges them in the units' order.
+#pragma once
+
+#include "chunk.cuh"
+#include "umma.cuh"
+
+namespace adamas {
+
+constexpr int kAtThreads = 512;
+constexpr int kAtStages = 4;
+constexpr int kAtMaxGrid = 160;
+constexpr int kAtPartRow = 132;             // m, l, -, -, o[128]
+constexpr int64_t kAtL2Bytes = 48ll << 20;  // K and V of heads that go through a wave together
+
+// Plan of a launch, made by every block for itself (the lengths are on the device).
+struct AtPlan {
+  int mpre[kMaxBatch + 1];            // units of the sequences with several, before each
+  long long spre[kMaxBatch + 1];      // tiles of the sequences with one unit per head, before each
+  long long lpre[kAtMaxGrid + 1];            // tiles of the left-over units, before each
+  int first[kMaxBatch];               // the sequence's rows
+  int n[kMaxBatch];
+  int len[kMaxBatch];
+  long long W, Wl;   // tiles of the line, of its left-over units
+  int waves, left, shares;
+};
+
+constexpr size_t kAtSmem = 2 * kTileBytes + kAtStages * kTileBytes + 1024;
+
+struct AtParams {
+  ChunkParams c;
+  float* part;        // [2 * grid][part_rows][kAtPartRow]
+  uint32_t* arrived;  // [grid]
+  int part_rows;
+  int TQ;             // tokens of one 128-row tile
+};
+
+struct AtUnit {
+  int b, h, tok0, ntok;  // sequence, kv head, first new token, new tokens
+  int pos0;              // slot of the first token (may be negative)
+  int kv_end;            // slots that the last token sees
+  int tiles;
+};
+
+struct AtSegment {
+  AtUnit u;
+  int t0, t1;      // K/V tiles [t0, t1) of the unit
+  bool part;       // not the whole unit
+  int slot, ca, cb;  // partial state's place; blocks that share the unit
+};
+
+struct AtWalk {
+  int wave = 0;
+  long long x, x1;
+};
+
+__device__ __forceinline__ AtUnit at_unit(const AtPlan& pl, const AtParams& p, int b, int h, int qi) {
+  AtUnit u;
+  const int tu = 2 * p.TQ;
+  u.b = b;
+  u.h = h;
+  u.tok0 = qi * tu;
+  u.ntok = pl.n[b] - u.tok0 < tu ? pl.n[b] - u.tok0 : tu;
+  u.pos0 = pl.len[b] - pl.n[b] + u.tok0;
+  const int end = u.pos0 + u.ntok;
+  u.kv_end = end < 0 ? 0 : end;
+  u.tiles = u.kv_end == 0 ? 1 : (u.kv_end + 127) / 128;
+  return u;
+}
+
+// unit number u of the sequences with several: by groups of heads whose K and V fit in
+// L2, then from the chunk's last tokens (the longest) to its first
+__device__ __forceinline__ AtUnit at_multi_unit(const AtPlan& pl, const AtParams& p, int u) {
+  int lo = 0, hi = p.c.B;  // mpre[lo] <= u < mpre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pl.mpre[mid] <= u) lo = mid;
+    else hi = mid;
+  }
+  const int Hkv = p.c.Hkv, local = u - pl.mpre[lo], nu = (pl.mpre[hi] - pl.mpre[lo]) / Hkv;
+  int64_t hg = kAtL2Bytes / ((int64_t)(pl.len[lo] > 0 ? pl.len[lo] : 1) * 4 * kDim);
+  hg = hg < 1 ? 1 : (hg > Hkv ? Hkv : hg);
+  const int per = nu * (int)hg, gi = local / per, rem = local - gi * per;
+  const int hc = Hkv - gi * (int)hg < (int)hg ? Hkv - gi * (int)hg : (int)hg;
+  const int q = rem / hc;
+  return at_unit(pl, p, lo, gi * (int)hg + (rem - q * hc), nu - 1 - q);
+}
+
+__device__ __forceinline__ bool at_next(const AtPlan& pl, const AtParams& p, AtWalk& w, AtSegment& s) {
+  const int n = gridDim.x, c = blockIdx.x;
+  if (w.wave < pl.waves) {
+    s.u = at_multi_unit(pl, p, w.wave * n + ((w.wave & 1) ? n - 1 - c : c));
+    ++w.wave;
+    s.t0 = 0;
+    s.t1 = s.u.tiles;
+    s.part = false;
+    return true;
+  }
+  if (w.x >= w.x1) return false;
+  long long f0, f1;
+  if (w.x < pl.Wl) {
+    int lo = 0, hi = pl.left;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pl.lpre[mid] <= w.x) lo = mid;
+      else hi = mid;
+    }
+    s.u = at_multi_unit(pl, p, pl.waves * n + lo);
+    f0 = pl.lpre[lo];
+    f1 = pl.lpre[lo + 1];
+  } else {
+    const long long y = w.x - pl.Wl;
+    int lo = 0, hi = p.c.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pl.spre[mid] <= y) lo = mid;
+      else hi = mid;
+    }
+    const int tiles = (int)((pl.spre[hi] - pl.spre[lo]) / p.c.Hkv);
+    const int h = (int)((y - pl.spre[lo]) / tiles);
+    s.u = at_unit(pl, p, lo, h, 0);
+    f0 = pl.Wl + pl.spre[lo] + (long long)h * tiles;
+    f1 = f0 + tiles;
+  }
+  s.t0 = (int)(w.x - f0);
+  const long long e = w.x1 < f1 ? w.x1 : f1;
+  s.t1 = (int)(e - f0);
+  w.x = e;
+  s.part = s.t0 != 0 || e != f1;
+  s.slot = 2 * c + (s.t0 == 0 ? 1 : 0);
+  if (s.part) {  // the blocks whose shares hold the unit's first and last tile
+    s.ca = (int)(((f0 + 1) * pl.shares - 1) / pl.W);
+    s.cb = (int)((f1 * pl.shares - 1) / pl.W);
+  }
+  return true;
+}
+
+__device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, int tid) {
+  const int B = p.c.B, tu = 2 * p.TQ;
+  bool bad_cu = false, bad_len = false;
+  for (int b = tid; b < B; b += kAtThreads) {
+    int first, n;
+    ragged_rows(p.c.cu_q, b, p.c.T, first, n, bad_cu);
+    pl.first[b] = first;
+    pl.n[b] = n;
+    pl.len[b] = (int)clamp_len(p.c.seq_lens[b], p.c.geo.Nmax, bad_len);
+  }
+  if (bad_cu) atomicOr(p.c.err, kErrOffsets);
+  if (bad_len) atomicOr(p.c.err, kErrSeqLen);
+  __syncthreads();
+  if (tid < 32) {
+    int mu = 0;
+    long long st = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      const int b = b0 + tid;
+      int m = 0;
+      long long s = 0;
+      if (b < B && pl.n[b] > 0) {
+        const int nu = (pl.n[b] + tu - 1) / tu;
+        if (nu > 1) m = nu * p.c.Hkv;
+        else s = (long long)p.c.Hkv * (pl.len[b] == 0 ? 1 : (pl.len[b] + 127) / 128);
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int mm = __shfl_up_sync(0xffffffffu, m, d);
+        const long long ss = __shfl_up_sync(0xffffffffu, s, d);
+        if (tid >= d) {
+          m += mm;
+          s += ss;
+        }
+      }
+      if (b < B) {
+        pl.mpre[b + 1] = mu + m;
+        pl.spre[b + 1] = st + s;
+      }
+      mu += __shfl_sync(0xffffffffu, m, 31);
+      st += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (tid == 0) {
+      pl.mpre[0] = 0;
+      pl.spre[0] = 0;
+      pl.waves = mu / (int)gridDim.x;
+      pl.left = mu - pl.waves * (int)gridDim.x;
+    }
+  }
+  __syncthreads();
+  if (tid < pl.left) pl.lpre[tid + 1] = at_multi_unit(pl, p, pl.waves * (int)gridDim.x + tid).tiles;
+  __syncthreads();
+  if (tid == 0) {
+    long long s = 0;
+    pl.lpre[0] = 0;
+    for (int i = 1; i <= pl.left; ++i) {
+      s += pl.lpre[i];
+      pl.lpre[i] = s;
+    }
+    pl.Wl = s;
+    pl.W = s + pl.spre[B];
+    pl.shares = pl.W < (long long)gridDim.x ? (int)pl.W : (int)gridDim.x;  // no share is empty
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ AtWalk at_start(const AtPlan& pl) {
+  AtWalk w;
+  const int c = blockIdx.x;
+  w.x = c < pl.shares ? pl.W * c / pl.shares : 0;
+  w.x1 = c < pl.shares ? pl.W * (c + 1) / pl.shares : 0;
+  return w;
+}
+
+__global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ AtPlan pl;
+  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], kv_full[kAtStages],
+      kv_empty[kAtStages], all_done;
+  __shared__ uint32_t tmem_slot, gave_up, last_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t q_tile = base, ring = base + 2 * kTileBytes;
+
+  if (tid == 0) {
+    mbar_init(&q_full, 4);
+    mbar_init(&q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+      mbar_init(&o_full[t], 1);
+    }
+    for (int i = 0; i < kAtStages; ++i) {
+      mbar_init(&kv_full[i], 4);
+      mbar_init(&kv_empty[i], 1);
+    }
+    mbar_init(&all_done, 1);
+    gave_up = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) tmem_alloc512(&tmem_slot);
+  tmem_fence_before();
+  at_make_plan(pl, p, tid);  // ends with a barrier of the block
+  tmem_fence_after();
+  const uint32_t tmem = tmem_slot;  // columns: S0 | S1 | O0 | O1, 128 each
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    const int t = warp >> 2;                      // tile
+    const int r = (warp & 3) * 32 + lane;         // row of the tile
+    const uint32_t quad = (uint32_t)(warp & 3) << 21;  // 32 lanes, in the address's upper half
+    const uint32_t S = tmem + quad + 128 * t, O = tmem + quad + 256 + 128 * t;
+    const int G = p.c.G, rt = r / G, rg = r - rt * G;  // the row's token in the tile, its head in the group
+    AtWalk w = at_start(pl);
+    AtSegment sg;
+    uint32_t s_par = 0, o_par = 0;
+    while (at_next(pl, p, w, sg)) {
+      const int tok = t * p.TQ + rt;
+      const int rows = (sg.u.ntok - t * p.TQ) * G;  // live rows of the tile (may be below 0 or above 128)
+      if (rows > 0) {
+        const bool live = rt < p.TQ && tok < sg.u.ntok;
+        const bool warp_live = (warp & 3) * 32 < rows;
+        const int vis = live ? (sg.u.pos0 + tok + 1 < 0 ? 0 : sg.u.pos0 + tok + 1) : 0;  // slots it sees
+        // all rows of the warp see at least this many (dead rows aside)
+        const int vis_all = __reduce_min_sync(0xffffffffu, live ? vis : 0x7fffffff);
+        float m = -INFINITY, l = 0.0f;
+        for (int j = sg.t0; j < sg.t1; ++j) {
+          mbar_wait_or_give_up(&s_full[t], s_par, &gave_up);
+          s_par ^= 1;
+          if (warp_live) {
+            tmem_fence_after();
+            float s[128];
+            {
+              uint32_t x[4][32];
+              tmem_ld32(S, x[0]);
+              tmem_ld32(S + 32, x[1]);
+              tmem_ld32(S + 64, x[2]);
+              tmem_ld32(S + 96, x[3]);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(x[i >> 5][i & 31]);
+            }
+            if (j * 128 + 128 > vis_all) {
+              const int seen = vis - j * 128;
+#pragma unroll
+              for (int i = 0; i < 128; ++i) s[i] = i < seen ? s[i] : -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int i = 4; i < 128; i += 8) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(s[i + k], i + 4 + k < 128 ? s[i + 4 + k] : s[i + k]));
+            }
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScoreLog2;
+            const bool raise = mt > m + 8.0f;  // also when m is -inf and a score is not
+            if (__any_sync(0xffffffffu, raise)) {
+              const float mn = raise ? mt : m;
+              const float f = raise ? fast_exp2(m - mn) : 1.0f;  // 0 when m was -inf
+              m = mn;
+              l *= f;
+              if (j > sg.t0) {  // every product into O is done: S of this tile came after them
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                  uint32_t x[32];
+                  tmem_ld32(O + c, x);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                  tmem_st32(O + c, x);
+                }
+              }
+            }
+            const float sub = m == -INFINITY ? 0.0f : m;
+            float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              uint32_t x[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float a = fast_exp2(fmaf(s[64 * hf + 2 * i], kScoreLog2, -sub));
+                const float b = fast_exp2(fmaf(s[64 * hf + 2 * i + 1], kScoreLog2, -sub));
+                sum[i & 1] += a;
+                sum[2 + (i & 1)] += b;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[i]) : "f"(b), "f"(a));
+              }
+              tmem_st32(S + 32 * hf, x);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st();
+            tmem_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[t]);
+        }
+        // ---- epilogue
+        mbar_wait_or_give_up(&o_full[t], o_par, &gave_up);
+        o_par ^= 1;
+        if (warp_live) {
+          tmem_fence_after();
+          const int64_t row = (int64_t)(pl.first[sg.u.b] + sg.u.tok0 + tok) * p.c.Hq + sg.u.h * G + rg;
+          if (!sg.part) {
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t x[32];
+              tmem_ld32(O + c, x);
+              tmem_wait_ld();
+              if (live) {
+                uint32_t y[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float a = __uint_as_float(x[2 * i]) * inv, b = __uint_as_float(x[2 * i + 1]) * inv;
+                  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[i]) : "f"(l > 0.0f ? b : 0.0f), "f"(l > 0.0f ? a : 0.0f));
+                }
+                uint4* o = reinterpret_cast<uint4*>(p.c.out + row * kDim + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+              }
+            }
+            if (live && p.c.lse)
+              p.c.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          } else {
+            // rows of a partial state: token-major over both tiles
+            const int prow = tok * G + rg;
+            float* st = p.part + ((int64_t)sg.slot * p.part_rows + prow) * kAtPartRow;
+            if (live) *reinterpret_cast<float2*>(st) = make_float2(m, l);
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t x[32];
+              tmem_ld32(O + c, x);
+              tmem_wait_ld();
+              if (live) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  reinterpret_cast<uint4*>(st + 4 + c)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+              }
+            }
+          }
+          tmem_fence_before();
+        }
+      }
+      if (sg.part) {
+        // the last of the unit's blocks to arrive merges the states, in the blocks' order
+        __threadfence();
+        named_sync(1, 256);
+        if (tid == 0) {
+          const uint32_t before = atomicAdd(&p.arrived[sg.ca], 1u);
+          last_flag = before == (uint32_t)(sg.cb - sg.ca);
+          if (last_flag) p.arrived[sg.ca] = 0;
+        }
+        named_sync(1, 256);
+        if (last_flag) {
+          __threadfence();
+          const int rows_all = sg.u.ntok * G;
+          for (int pr = warp; pr < rows_all; pr += 8) {
+            float M = -INFINITY;
+            for (int c = sg.ca; c <= sg.cb; ++c)
+              M = fmaxf(M, __ldcg(p.part + ((int64_t)(2 * c + (c == sg.ca)) * p.part_rows + pr) * kAtPartRow));
+            float L = 0.0f;
+            float4 o = make_float4(0, 0, 0, 0);
+            if (M != -INFINITY) {
+              for (int c = sg.ca; c <= sg.cb; ++c) {
+                const float* st = p.part + ((int64_t)(2 * c + (c == sg.ca)) * p.part_rows + pr) * kAtPartRow;
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(st));
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(st + 4) + lane);
+                if (ml.x == -INFINITY) continue;
+                const float f = fast_exp2(ml.x - M);
+                L += ml.y * f;
+                o.x += x.x * f;
+                o.y += x.y * f;
+                o.z += x.z * f;
+                o.w += x.w * f;
+              }
+            }
+            const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+            const int tk = pr / G;
+            const int64_t row = (int64_t)(pl.first[sg.u.b] + sg.u.tok0 + tk) * p.c.Hq + sg.u.h * G + (pr - tk * G);
+            uint32_t y0, y1;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y0) : "f"(o.y * inv), "f"(o.x * inv));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y1) : "f"(o.w * inv), "f"(o.z * inv));
+            reinterpret_cast<uint2*>(p.c.out + row * kDim)[lane] = make_uint2(y0, y1);
+            if (lane == 0 && p.c.lse) p.c.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+          }
+        }
+        named_sync(1, 256);  // last_flag is read before the next unit sets it
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp < 12) {
+      // ---------------------------------------------------------- copies
+      const int lt = tid - 256, lr = lt >> 4, lc = lt & 15;  // rows lr + 8 i, piece lc
+      const uint32_t piece = tile_piece(lr, lc);             // rows 8 apart share the exchange: + 1024 i
+      AtWalk w = at_start(pl);
+      AtSegment sg;
+      uint32_t it = 0, nseg = 0;
+      bool bad = false;
+      // Copies in flight, oldest first (their barriers are told when they have landed).
+      uint64_t *b0 = nullptr, *b1 = nullptr, *b2 = nullptr;
+      int inflight = 0;
+      auto landed = [&]() {  // the oldest copies are in shared memory: make the products' proxy see them
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b0);
+        b0 = b1;
+        b1 = b2;
+        --inflight;
+      };
+      auto flush = [&]() {
+        if (inflight == 3) cp_async_wait<2>();
+        else if (inflight == 2) cp_async_wait<1>();
+        else cp_async_wait<0>();
+        landed();
+      };
+      auto push = [&](uint64_t* bar) {
+        cp_async_commit();
+        if (inflight == 3) {
+          cp_async_wait<3>();
+          landed();
+        }
+        if (inflight == 0) b0 = bar;
+        else if (inflight == 1) b1 = bar;
+        else b2 = bar;
+        ++inflight;
+      };
+      // A buffer that is not free yet may be waiting for copies that have landed unseen:
+      // hand those over, oldest first, before waiting for it.
+      auto acquire = [&](uint64_t* bar, uint32_t parity) {
+        while (!__all_sync(0xffffffffu, mbar_try(bar, parity))) {
+          if (inflight == 0) {
+            mbar_wait_or_give_up(bar, parity, &gave_up);
+            __syncwarp();
+            return;
+          }
+          flush();
+        }
+      };
+      while (at_next(pl, p, w, sg)) {
+        // Q: the live rows of both tiles
+        acquire(&q_empty, (nseg & 1) ^ 1);
+        ++nseg;
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+          int rows = (sg.u.ntok - t * p.TQ) * p.c.G;
+          if (rows > p.TQ * p.c.G) rows = p.TQ * p.c.G;
+          const uint16_t* q = p.c.q + (int64_t)(pl.first[sg.u.b] + sg.u.tok0 + t * p.TQ) * p.c.Hq * kDim +
+                              (int64_t)sg.u.h * p.c.G * kDim + lc * 8;
+#pragma unroll 1
+          for (int r = lr; r < rows; r += 8) {
+            const int tk = r / p.c.G;
+            cp_async16_or_zero(q_tile + t * kTileBytes + piece + (r - lr) * 128,
+                               q + ((int64_t)tk * p.c.Hq + (r - tk * p.c.G)) * kDim, true);
+          }
+        }
+        push(&q_full);
+        for (int j = sg.t0; j < sg.t1; ++j) {
+          // the tile's rows, 16 per thread
+          uint32_t row[16];
+          const int tb = j * 128 + lr;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int tk = tb + 8 * i;
+            row[i] = tk < sg.u.kv_end ? p.c.geo.row32(sg.u.b, sg.u.h, tk, bad) : 0u;
+          }
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv, ++it) {
+            const int stage = it % kAtStages;
+            acquire(&kv_empty[stage], ((it / kAtStages) & 1) ^ 1);
+            const uint16_t* src = (kv ? p.c.V : p.c.K) + lc * 8;
+            const uint32_t dst = ring + stage * kTileBytes + piece;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              cp_async16_or_zero(dst + 1024 * i, src + (int64_t)row[i] * kDim, tb + 8 * i < sg.u.kv_end);
+            push(&kv_full[stage]);
+          }
+        }
+      }
+      while (inflight > 0) flush();
+      if (bad) atomicOr(p.c.err, kErrTable);
+    } else if (warp == 12) {
+      // ---------------------------------------------------------- products
+      if (lane == 0) {
+        AtWalk w = at_start(pl);
+        AtSegment sg;
+        uint32_t it = 0, nseg = 0, p_par[2] = {0, 0};
+        auto kv_wait = [&](uint32_t i) {
+          mbar_wait_or_give_up(&kv_full[i % kAtStages], (i / kAtStages) & 1, &gave_up);
+        };
+        while (at_next(pl, p, w, sg)) {
+          const int nt = sg.u.ntok > p.TQ ? 2 : 1;
+          mbar_wait_or_give_up(&q_full, nseg & 1, &gave_up);
+          ++nseg;
+          kv_wait(it);
+          tmem_fence_after();
+          for (int t = 0; t < nt; ++t) {
+            mma_rows_rows(tmem + 128 * t, q_tile + t * kTileBytes, ring + (it % kAtStages) * kTileBytes);
+            mma_commit(&s_full[t]);
+          }
+          mma_commit(&kv_empty[it % kAtStages]);
+          for (int j = sg.t0; j < sg.t1; ++j, it += 2) {
+            const bool more = j + 1 < sg.t1;
+            const uint32_t vs = (it + 1) % kAtStages, ks = (it + 2) % kAtStages;
+            kv_wait(it + 1);
+            if (more) kv_wait(it + 2);
+            for (int t = 0; t < nt; ++t) {
+              mbar_wait_or_give_up(&p_full[t], p_par[t], &gave_up);
+              p_par[t] ^= 1;
+              tmem_fence_after();
+              mma_probs_rows(tmem + 256 + 128 * t, tmem + 128 * t, ring + vs * kTileBytes, j > sg.t0);
+              if (more) {
+                mma_rows_rows(tmem + 128 * t, q_tile + t * kTileBytes, ring + ks * kTileBytes);
+                mma_commit(&s_full[t]);
+              } else {
+                mma_commit(&o_full[t]);
+              }
+            }
+            mma_commit(&kv_empty[vs]);
+            if (more) mma_commit(&kv_empty[ks]);
+          }
+          mma_commit(&q_empty);
+        }
+        mma_commit(&all_done);
+        mbar_wait_or_give_up(&all_done, 0, &gave_up);
+      }
+      __syncwarp();
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (warp == 12) tmem_free512(tmem);
+  if (tid == 0 && gave_up) atomicOr(p.c.err, kErrTimeout);
+}
+
+}  // namespace adamas
