@@ -11,9 +11,11 @@
 // and bf16's range.
 //
 // Roles: warps 0-3 and 4-7 one row per thread of tile 0 and 1 (softmax, rescaling,
-// epilogue); warps 8-11 copy Q, K and V rows through the block table with cp.async
-// (any page size, tails filled with zeros); one thread of warp 12 issues the products.
-// While one tile's softmax runs, the other tile's products do.
+// epilogue); warps 8-9 copy Q and K rows, warps 10-11 V rows, through the block table
+// with cp.async (any page size, tails filled with zeros); one thread of warp 12 issues
+// the products.  While one tile's softmax runs, the other tile's products do.  A unit of
+// one row tile (decode) takes its K/V tiles in turn as tile 0 and tile 1 -- the second
+// copy of S and O would idle otherwise -- and merges the two states at its end.
 //
 // Work split.  Sequences with several units (prompts) fill whole waves of the grid,
 // heads that fit in L2 together next to each other and the longest units first, so that
@@ -29,7 +31,7 @@
 namespace adamas {
 
 constexpr int kAtThreads = 512;
-constexpr int kAtStages = 4;
+constexpr int kAtStages = 2;  // of K, and of V
 constexpr int kAtMaxGrid = 160;
 constexpr int kAtPartRow = 132;             // m, l, -, -, o[128]
 constexpr int64_t kAtL2Bytes = 48ll << 20;  // K and V of heads that go through a wave together
@@ -46,7 +48,7 @@ struct AtPlan {
   int waves, left, shares;
 };
 
-constexpr size_t kAtSmem = 2 * kTileBytes + kAtStages * kTileBytes + 1024;
+constexpr size_t kAtSmem = 2 * kTileBytes + 2 * kAtStages * kTileBytes + 1024;
 
 struct AtParams {
   ChunkParams c;
@@ -232,15 +234,16 @@ __device__ __forceinline__ AtWalk at_start(const AtPlan& pl) {
 __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtParams p) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ AtPlan pl;
-  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], kv_full[kAtStages],
-      kv_empty[kAtStages], all_done;
+  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], k_full[kAtStages],
+      k_empty[kAtStages], v_full[kAtStages], v_empty[kAtStages], all_done;
+  __shared__ float2 duo[128];  // state of the second half of a one-tile unit
   __shared__ uint32_t tmem_slot, gave_up, last_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t q_tile = base, ring = base + 2 * kTileBytes;
+  const uint32_t q_tile = base, k_ring = base + 2 * kTileBytes, v_ring = k_ring + kAtStages * kTileBytes;
 
   if (tid == 0) {
-    mbar_init(&q_full, 4);
+    mbar_init(&q_full, 64);
     mbar_init(&q_empty, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
@@ -248,8 +251,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
       mbar_init(&o_full[t], 1);
     }
     for (int i = 0; i < kAtStages; ++i) {
-      mbar_init(&kv_full[i], 4);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&k_full[i], 64);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 64);
+      mbar_init(&v_empty[i], 1);
     }
     mbar_init(&all_done, 1);
     gave_up = 0;
@@ -273,16 +278,18 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
     AtSegment sg;
     uint32_t s_par = 0, o_par = 0;
     while (at_next(pl, p, w, sg)) {
-      const int tok = t * p.TQ + rt;
-      const int rows = (sg.u.ntok - t * p.TQ) * G;  // live rows of the tile (may be below 0 or above 128)
-      if (rows > 0) {
+      const bool two = sg.u.ntok > p.TQ;           // two row tiles, or one whose K/V tiles alternate
+      const int tok = two ? t * p.TQ + rt : rt;
+      const int rows = (sg.u.ntok - (two ? t * p.TQ : 0)) * G;  // live rows of the tile (may be above 128)
+      const int step = two ? 1 : 2, j0 = two ? sg.t0 : sg.t0 + t;
+      if (j0 < sg.t1) {
         const bool live = rt < p.TQ && tok < sg.u.ntok;
         const bool warp_live = (warp & 3) * 32 < rows;
         const int vis = live ? (sg.u.pos0 + tok + 1 < 0 ? 0 : sg.u.pos0 + tok + 1) : 0;  // slots it sees
         // all rows of the warp see at least this many (dead rows aside)
         const int vis_all = __reduce_min_sync(0xffffffffu, live ? vis : 0x7fffffff);
         float m = -INFINITY, l = 0.0f;
-        for (int j = sg.t0; j < sg.t1; ++j) {
+        for (int j = j0; j < sg.t1; j += step) {
           mbar_wait_or_give_up(&s_full[t], s_par, &gave_up);
           s_par ^= 1;
           if (warp_live) {
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
               const float f = raise ? fast_exp2(m - mn) : 1.0f;  // 0 when m was -inf
               m = mn;
               l *= f;
-              if (j > sg.t0) {  // every product into O is done: S of this tile came after them
+              if (j > j0) {  // every product into O is done: S of this tile came after them
 #pragma unroll 1
                 for (int c = 0; c < 128; c += 32) {
                   uint32_t x[32];
@@ -353,49 +360,77 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
         // ---- epilogue
         mbar_wait_or_give_up(&o_full[t], o_par, &gave_up);
         o_par ^= 1;
-        if (warp_live) {
-          tmem_fence_after();
-          const int64_t row = (int64_t)(pl.first[sg.u.b] + sg.u.tok0 + tok) * p.c.Hq + sg.u.h * G + rg;
-          if (!sg.part) {
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-              uint32_t x[32];
-              tmem_ld32(O + c, x);
-              tmem_wait_ld();
-              if (live) {
-                uint32_t y[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float a = __uint_as_float(x[2 * i]) * inv, b = __uint_as_float(x[2 * i + 1]) * inv;
-                  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[i]) : "f"(l > 0.0f ? b : 0.0f), "f"(l > 0.0f ? a : 0.0f));
-                }
-                uint4* o = reinterpret_cast<uint4*>(p.c.out + row * kDim + c);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-              }
-            }
-            if (live && p.c.lse)
-              p.c.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-          } else {
-            // rows of a partial state: token-major over both tiles
-            const int prow = tok * G + rg;
-            float* st = p.part + ((int64_t)sg.slot * p.part_rows + prow) * kAtPartRow;
-            if (live) *reinterpret_cast<float2*>(st) = make_float2(m, l);
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-              uint32_t x[32];
-              tmem_ld32(O + c, x);
-              tmem_wait_ld();
-              if (live) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  reinterpret_cast<uint4*>(st + 4 + c)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-              }
+        tmem_fence_after();
+        const bool merge = !two && sg.t1 - sg.t0 > 1;
+        float fa = 1.0f, fb = 0.0f;  // factors of this state and of the other one
+        if (merge) {
+          // tile 1's threads hand their maximum and sum to tile 0's, whose threads read both O
+          if (t == 1) {
+            duo[r] = make_float2(m, l);
+            tmem_fence_before();
+          }
+          named_sync(2, 256);
+          if (t == 0) {
+            tmem_fence_after();
+            const float2 other = duo[r];
+            const float M = fmaxf(m, other.x);
+            if (M != -INFINITY) {
+              fa = fast_exp2(m - M);
+              fb = fast_exp2(other.x - M);
+              l = l * fa + other.y * fb;
+              m = M;
             }
           }
-          tmem_fence_before();
         }
+        if (warp_live && !(merge && t == 1)) {
+          const int64_t row = (int64_t)(pl.first[sg.u.b] + sg.u.tok0 + tok) * p.c.Hq + sg.u.h * G + rg;
+          float* st = p.part + ((int64_t)sg.slot * p.part_rows + (tok * G + rg)) * kAtPartRow;
+          if (!sg.part) {
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;  // a row that sees nothing: O is 0 as well
+            fa *= inv;
+            fb *= inv;
+          }
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t x[32];
+            tmem_ld32(O + c, x);
+            tmem_wait_ld();
+            if (merge) {
+              uint32_t y[32];
+              tmem_ld32(O + 128 + c, y);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                x[i] = __float_as_uint(__uint_as_float(x[i]) * fa + __uint_as_float(y[i]) * fb);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fa);
+            }
+            if (!live) continue;
+            if (!sg.part) {
+              uint32_t y[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                    : "=r"(y[i])
+                    : "f"(__uint_as_float(x[2 * i + 1])), "f"(__uint_as_float(x[2 * i])));
+              uint4* o = reinterpret_cast<uint4*>(p.c.out + row * kDim + c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<uint4*>(st + 4 + c)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+          }
+          if (live) {
+            if (sg.part) *reinterpret_cast<float2*>(st) = make_float2(m, l);
+            else if (p.c.lse) p.c.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          }
+        }
+        tmem_fence_before();
+        // tile 0 has read both O before tile 1 lets the next products into its own
+        if (merge) named_sync(2, 256);
       }
       if (sg.part) {
         // the last of the unit's blocks to arrive merges the states, in the blocks' order
@@ -447,133 +482,117 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp < 12) {
       // ---------------------------------------------------------- copies
-      const int lt = tid - 256, lr = lt >> 4, lc = lt & 15;  // rows lr + 8 i, piece lc
-      const uint32_t piece = tile_piece(lr, lc);             // rows 8 apart share the exchange: + 1024 i
+      const bool is_v = warp >= 10;
+      const int lt = (tid - 256) & 63, lr = lt >> 4, lc = lt & 15;  // rows lr + 4 i, piece lc
+      const uint32_t piece[2] = {tile_piece(lr, lc), tile_piece(lr + 4, lc)};  // then + 1024 every 8 rows
+      const uint16_t* rows_of = (is_v ? p.c.V : p.c.K) + lc * 8;
+      const uint32_t ring = is_v ? v_ring : k_ring;
+      uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
       AtWalk w = at_start(pl);
       AtSegment sg;
       uint32_t it = 0, nseg = 0;
       bool bad = false;
-      // Copies in flight, oldest first (their barriers are told when they have landed).
-      uint64_t *b0 = nullptr, *b1 = nullptr, *b2 = nullptr;
-      int inflight = 0;
-      auto landed = [&]() {  // the oldest copies are in shared memory: make the products' proxy see them
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b0);
-        b0 = b1;
-        b1 = b2;
-        --inflight;
-      };
-      auto flush = [&]() {
-        if (inflight == 3) cp_async_wait<2>();
-        else if (inflight == 2) cp_async_wait<1>();
-        else cp_async_wait<0>();
-        landed();
-      };
-      auto push = [&](uint64_t* bar) {
-        cp_async_commit();
-        if (inflight == 3) {
-          cp_async_wait<3>();
-          landed();
-        }
-        if (inflight == 0) b0 = bar;
-        else if (inflight == 1) b1 = bar;
-        else b2 = bar;
-        ++inflight;
-      };
-      // A buffer that is not free yet may be waiting for copies that have landed unseen:
-      // hand those over, oldest first, before waiting for it.
-      auto acquire = [&](uint64_t* bar, uint32_t parity) {
-        while (!__all_sync(0xffffffffu, mbar_try(bar, parity))) {
-          if (inflight == 0) {
-            mbar_wait_or_give_up(bar, parity, &gave_up);
-            __syncwarp();
-            return;
-          }
-          flush();
-        }
-      };
       while (at_next(pl, p, w, sg)) {
-        // Q: the live rows of both tiles
-        acquire(&q_empty, (nseg & 1) ^ 1);
-        ++nseg;
+        if (!is_v) {  // Q: the live rows of both tiles
+          mbar_wait_or_give_up(&q_empty, (nseg & 1) ^ 1, &gave_up);
+          ++nseg;
 #pragma unroll 1
-        for (int t = 0; t < 2; ++t) {
-          int rows = (sg.u.ntok - t * p.TQ) * p.c.G;
-          if (rows > p.TQ * p.c.G) rows = p.TQ * p.c.G;
-          const uint16_t* q = p.c.q + (int64_t)(pl.first[sg.u.b] + sg.u.tok0 + t * p.TQ) * p.c.Hq * kDim +
-                              (int64_t)sg.u.h * p.c.G * kDim + lc * 8;
+          for (int t = 0; t < 2; ++t) {
+            int rows = (sg.u.ntok - t * p.TQ) * p.c.G;
+            if (rows > p.TQ * p.c.G) rows = p.TQ * p.c.G;
+            const uint16_t* q = p.c.q + (int64_t)(pl.first[sg.u.b] + sg.u.tok0 + t * p.TQ) * p.c.Hq * kDim +
+                                (int64_t)sg.u.h * p.c.G * kDim + lc * 8;
 #pragma unroll 1
-          for (int r = lr; r < rows; r += 8) {
-            const int tk = r / p.c.G;
-            cp_async16_or_zero(q_tile + t * kTileBytes + piece + (r - lr) * 128,
-                               q + ((int64_t)tk * p.c.Hq + (r - tk * p.c.G)) * kDim, true);
+            for (int r = lr; r < rows; r += 4) {
+              const int tk = r / p.c.G;
+              cp_async16_or_zero(q_tile + t * kTileBytes + tile_piece(r, lc),
+                                 q + ((int64_t)tk * p.c.Hq + (r - tk * p.c.G)) * kDim, true);
+            }
           }
+          cp_async_arrive(&q_full);
         }
-        push(&q_full);
-        for (int j = sg.t0; j < sg.t1; ++j) {
-          // the tile's rows, 16 per thread
-          uint32_t row[16];
+        for (int j = sg.t0; j < sg.t1; ++j, ++it) {
+          const int stage = it % kAtStages;
+          const uint32_t dst = ring + stage * kTileBytes;
           const int tb = j * 128 + lr;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int tk = tb + 8 * i;
-            row[i] = tk < sg.u.kv_end ? p.c.geo.row32(sg.u.b, sg.u.h, tk, bad) : 0u;
-          }
 #pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++it) {
-            const int stage = it % kAtStages;
-            acquire(&kv_empty[stage], ((it / kAtStages) & 1) ^ 1);
-            const uint16_t* src = (kv ? p.c.V : p.c.K) + lc * 8;
-            const uint32_t dst = ring + stage * kTileBytes + piece;
+          for (int hf = 0; hf < 2; ++hf) {  // rows 64 hf + lr + 4 i
+            uint32_t row[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int tk = tb + 64 * hf + 4 * i;
+              row[i] = tk < sg.u.kv_end ? p.c.geo.row32(sg.u.b, sg.u.h, tk, bad) : 0u;
+            }
+            if (hf == 0) mbar_wait_or_give_up(&empty[stage], ((it / kAtStages) & 1) ^ 1, &gave_up);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              cp_async16_or_zero(dst + 1024 * i, src + (int64_t)row[i] * kDim, tb + 8 * i < sg.u.kv_end);
-            push(&kv_full[stage]);
+              cp_async16_or_zero(dst + piece[i & 1] + 8192 * hf + 1024 * (i >> 1), rows_of + (int64_t)row[i] * kDim,
+                                 tb + 64 * hf + 4 * i < sg.u.kv_end);
           }
+          cp_async_arrive(&full[stage]);
         }
       }
-      while (inflight > 0) flush();
+      cp_async_wait<0>();
       if (bad) atomicOr(p.c.err, kErrTable);
     } else if (warp == 12) {
       // ---------------------------------------------------------- products
       if (lane == 0) {
         AtWalk w = at_start(pl);
         AtSegment sg;
-        uint32_t it = 0, nseg = 0, p_par[2] = {0, 0};
-        auto kv_wait = [&](uint32_t i) {
-          mbar_wait_or_give_up(&kv_full[i % kAtStages], (i / kAtStages) & 1, &gave_up);
+        uint32_t ik = 0, iv = 0, nseg = 0, p_par[2] = {0, 0};
+        // K tile -> S of t for the row tiles of the unit (or its only one)
+        auto scores = [&](int t, int qt) {
+          mma_rows_rows(tmem + 128 * t, q_tile + qt * kTileBytes, k_ring + (ik % kAtStages) * kTileBytes);
+          mma_commit(&s_full[t]);
+        };
+        auto k_wait = [&]() {
+          mbar_wait_or_give_up(&k_full[ik % kAtStages], (ik / kAtStages) & 1, &gave_up);
+          fence_async_smem();
+        };
+        auto k_next = [&]() { mma_commit(&k_empty[ik++ % kAtStages]); };
+        auto outputs = [&](int t, bool acc) {
+          mbar_wait_or_give_up(&p_full[t], p_par[t], &gave_up);
+          p_par[t] ^= 1;
+          tmem_fence_after();
+          mma_probs_rows(tmem + 256 + 128 * t, tmem + 128 * t, v_ring + (iv % kAtStages) * kTileBytes, acc);
         };
         while (at_next(pl, p, w, sg)) {
-          const int nt = sg.u.ntok > p.TQ ? 2 : 1;
+          const bool two = sg.u.ntok > p.TQ;
+          const int n = sg.t1 - sg.t0, ahead = two ? 1 : 2;  // K tiles whose scores are under way
           mbar_wait_or_give_up(&q_full, nseg & 1, &gave_up);
           ++nseg;
-          kv_wait(it);
-          tmem_fence_after();
-          for (int t = 0; t < nt; ++t) {
-            mma_rows_rows(tmem + 128 * t, q_tile + t * kTileBytes, ring + (it % kAtStages) * kTileBytes);
-            mma_commit(&s_full[t]);
+          for (int j = 0; j < ahead && j < n; ++j) {
+            k_wait();
+            tmem_fence_after();
+            scores(two ? 0 : j, 0);
+            if (two) scores(1, 1);
+            k_next();
           }
-          mma_commit(&kv_empty[it % kAtStages]);
-          for (int j = sg.t0; j < sg.t1; ++j, it += 2) {
-            const bool more = j + 1 < sg.t1;
-            const uint32_t vs = (it + 1) % kAtStages, ks = (it + 2) % kAtStages;
-            kv_wait(it + 1);
-            if (more) kv_wait(it + 2);
-            for (int t = 0; t < nt; ++t) {
-              mbar_wait_or_give_up(&p_full[t], p_par[t], &gave_up);
-              p_par[t] ^= 1;
-              tmem_fence_after();
-              mma_probs_rows(tmem + 256 + 128 * t, tmem + 128 * t, ring + vs * kTileBytes, j > sg.t0);
+          for (int j = 0; j < n; ++j) {
+            mbar_wait_or_give_up(&v_full[iv % kAtStages], (iv / kAtStages) & 1, &gave_up);
+            fence_async_smem();
+            const bool more = j + ahead < n;
+            if (two) {
+              if (more) k_wait();
+              for (int t = 0; t < 2; ++t) {
+                outputs(t, j > 0);
+                if (more) scores(t, t);
+                else mma_commit(&o_full[t]);
+              }
+              mma_commit(&v_empty[iv++ % kAtStages]);
+              if (more) k_next();
+            } else {
+              const int t = j & 1;
+              outputs(t, j > 1);
+              mma_commit(&v_empty[iv++ % kAtStages]);
               if (more) {
-                mma_rows_rows(tmem + 128 * t, q_tile + t * kTileBytes, ring + ks * kTileBytes);
-                mma_commit(&s_full[t]);
+                k_wait();
+                scores(t, 0);
+                k_next();
               } else {
                 mma_commit(&o_full[t]);
               }
             }
-            mma_commit(&kv_empty[vs]);
-            if (more) mma_commit(&kv_empty[ks]);
           }
           mma_commit(&q_empty);
         }

@@ -138,6 +138,12 @@ __device__ __forceinline__ void mbar_wait_or_give_up(uint64_t* bar, uint32_t par
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
+// The barrier is arrived at once when every cp.async this thread issued before has landed
+// (the arrival counts as one of those the barrier expects).  Whoever waits for it runs
+// fence_async_smem() before the tensor core reads what landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 __device__ __forceinline__ float fast_exp2(float x) {  // 2 ulp; 0 for -inf
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
