@@ -79,6 +79,41 @@ static int attend_device(int* sms) {
   return ADAMAS_OK;
 }
 
+// A tensor map over the rows of K or V: 128 columns in two boxes of 64 (128 bytes), `box`
+// rows each.  The encoder is a driver call, reached through the runtime.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static int rows_map(const void* base, int64_t rows, int box, CUtensorMap* map) {
+  static std::atomic<EncodeTiledFn> known{nullptr};
+  EncodeTiledFn fn = known.load(std::memory_order_acquire);
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (q != cudaDriverEntryPointSuccess || !f) return ADAMAS_ERR_UNSUPPORTED;
+    fn = reinterpret_cast<EncodeTiledFn>(f);
+    known.store(fn, std::memory_order_release);
+  }
+  const cuuint64_t dims[2] = {(cuuint64_t)kDim, (cuuint64_t)rows}, strides[1] = {2 * kDim};
+  const cuuint32_t boxes[2] = {64, (cuuint32_t)box}, steps[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, steps,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ADAMAS_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
+// Rows of one tensor-map copy of a 128-row tile: all of them, or the largest power of two
+// that divides the page size, of at least 8 rows (the swizzle's period); else 0.
+static int rows_box(const CacheGeom& g, int page_size) {
+  int box = 128;
+  if (g.table)
+    while (box >= 8 && page_size % box != 0) box >>= 1;
+  return box >= 8 ? box : 0;
+}
+
 // Workspace of chunk attention: control words | arrival counters | partial states.
 static int part_rows(int T, int G) {
   const int tu = 2 * (128 / G);
@@ -193,10 +228,18 @@ int adamas_chunk_attend(const adamas_chunk_args* args, adamas_stream_t stream) {
   ap.part = reinterpret_cast<float*>(ws + kCtrlBytes + kAtArrivedBytes);
   ap.part_rows = part_rows(a.T, p.G);
   ap.TQ = 128 / p.G;
+  const int64_t rows = a.block_table ? a.n_pages * p.Hkv * a.page_size : (int64_t)a.B * p.Hkv * p.geo.Nmax;
+  if (rows > INT32_MAX) return ADAMAS_ERR_UNSUPPORTED;
+  CUtensorMap k_map = {}, v_map = {};
+  ap.box = rows > 0 ? rows_box(p.geo, a.page_size) : 0;
+  if (ap.box && ((rc = rows_map(a.K, rows, ap.box, &k_map)) != ADAMAS_OK ||
+                 (rc = rows_map(a.V, rows, ap.box, &v_map)) != ADAMAS_OK))
+    return rc;
   // no more blocks than K/V tiles of all units
   const int64_t units = (int64_t)p.Hkv * ((a.T + 2 * ap.TQ - 1) / (2 * ap.TQ) + p.B);
   const int64_t tiles = units * ((p.geo.Nmax + 127) / 128 + 1);
-  chunk_attend_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kAtThreads, kAtSmem, (cudaStream_t)stream>>>(ap);
+  chunk_attend_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kAtThreads, kAtSmem, (cudaStream_t)stream>>>(ap, k_map,
+                                                                                                            v_map);
   return launched();
 }
 

@@ -10,10 +10,14 @@
 // quotient is the same for every choice of it, and P and the sum stay far from fp32's
 // and bf16's range.
 //
+// K and V tiles arrive by tensor-map copies of `box` rows -- all 128, or the largest
+// power of two of at least 8 rows that divides the page size -- one lane per page piece;
+// rows past the last visible slot are zeroed in V's tile (0 * NaN) and masked in S.  Page
+// sizes without such a divisor are copied row by row with cp.async, at a fifth of the rate.
+//
 // Roles: warps 0-3 and 4-7 one row per thread of tile 0 and 1 (softmax, rescaling,
-// epilogue); warps 8-9 copy Q and K rows, warps 10-11 V rows, through the block table
-// with cp.async (any page size, tails filled with zeros); one thread of warp 12 issues
-// the products.  While one tile's softmax runs, the other tile's products do.  A unit of
+// epilogue); warps 8-9 copy Q and K rows, warps 10-11 V rows, through the block table;
+// one thread of warp 12 issues the products.  While one tile's softmax runs, the other tile's products do.  A unit of
 // one row tile (decode) takes its K/V tiles in turn as tile 0 and tile 1 -- the second
 // copy of S and O would idle otherwise -- and merges the two states at its end.
 //
@@ -24,6 +28,8 @@
 // into equal shares, one per block: a unit cut by a share's end leaves partial states
 // in the workspace, and the block that arrives last merges them in the units' order.
 #pragma once
+
+#include <cuda.h>
 
 #include "chunk.cuh"
 #include "umma.cuh"
@@ -56,6 +62,7 @@ struct AtParams {
   uint32_t* arrived;  // [grid]
   int part_rows;
   int TQ;             // tokens of one 128-row tile
+  int box;            // rows of a tensor-map copy; 0: rows are copied one by one
 };
 
 struct AtUnit {
@@ -209,16 +216,25 @@ __device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, int 
   __syncthreads();
   if (tid < pl.left) pl.lpre[tid + 1] = at_multi_unit(pl, p, pl.waves * (int)gridDim.x + tid).tiles;
   __syncthreads();
-  if (tid == 0) {
-    long long s = 0;
-    pl.lpre[0] = 0;
-    for (int i = 1; i <= pl.left; ++i) {
-      s += pl.lpre[i];
-      pl.lpre[i] = s;
+  if (tid < 32) {
+    long long sum = 0;
+    for (int i0 = 1; i0 <= pl.left; i0 += 32) {
+      long long v = i0 + tid <= pl.left ? pl.lpre[i0 + tid] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, d);
+        if (tid >= d) v += u;
+      }
+      v += sum;
+      if (i0 + tid <= pl.left) pl.lpre[i0 + tid] = v;
+      sum = __shfl_sync(0xffffffffu, v, 31);
     }
-    pl.Wl = s;
-    pl.W = s + pl.spre[B];
-    pl.shares = pl.W < (long long)gridDim.x ? (int)pl.W : (int)gridDim.x;  // no share is empty
+    if (tid == 0) {
+      pl.lpre[0] = 0;
+      pl.Wl = sum;
+      pl.W = sum + pl.spre[B];
+      pl.shares = pl.W < (long long)gridDim.x ? (int)pl.W : (int)gridDim.x;  // no share is empty
+    }
   }
   __syncthreads();
 }
@@ -231,11 +247,13 @@ __device__ __forceinline__ AtWalk at_start(const AtPlan& pl) {
   return w;
 }
 
-__global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtParams p) {
+__global__ void __launch_bounds__(kAtThreads, 1)
+    chunk_attend_kernel(const AtParams p, const __grid_constant__ CUtensorMap k_map,
+                        const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ AtPlan pl;
   __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], k_full[kAtStages],
-      k_empty[kAtStages], v_full[kAtStages], v_empty[kAtStages], all_done;
+      k_empty[kAtStages], v_full[kAtStages], v_empty[kAtStages], v_tail, all_done;
   __shared__ float2 duo[128];  // state of the second half of a one-tile unit
   __shared__ uint32_t tmem_slot, gave_up, last_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -256,6 +274,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
       mbar_init(&v_full[i], 64);
       mbar_init(&v_empty[i], 1);
     }
+    mbar_init(&v_tail, 1);
     mbar_init(&all_done, 1);
     gave_up = 0;
     fence_mbar_init();
@@ -444,35 +463,49 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
         named_sync(1, 256);
         if (last_flag) {
           __threadfence();
+          // eight lanes a row, sixteen columns a lane, so that a warp has four rows' loads
+          // under way; the states one after the other, each joined by its weight
           const int rows_all = sg.u.ntok * G;
-          for (int pr = warp; pr < rows_all; pr += 8) {
-            float M = -INFINITY;
-            for (int c = sg.ca; c <= sg.cb; ++c)
-              M = fmaxf(M, __ldcg(p.part + ((int64_t)(2 * c + (c == sg.ca)) * p.part_rows + pr) * kAtPartRow));
-            float L = 0.0f;
-            float4 o = make_float4(0, 0, 0, 0);
-            if (M != -INFINITY) {
-              for (int c = sg.ca; c <= sg.cb; ++c) {
-                const float* st = p.part + ((int64_t)(2 * c + (c == sg.ca)) * p.part_rows + pr) * kAtPartRow;
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(st));
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(st + 4) + lane);
-                if (ml.x == -INFINITY) continue;
-                const float f = fast_exp2(ml.x - M);
-                L += ml.y * f;
-                o.x += x.x * f;
-                o.y += x.y * f;
-                o.z += x.z * f;
-                o.w += x.w * f;
+          const int64_t state = (int64_t)2 * p.part_rows * kAtPartRow;  // from one block's to the next one's
+          for (int pr = warp * 4 + (lane >> 3); pr < rows_all; pr += 32) {
+            // the first block's state is in its second place
+            const float* st = p.part + ((int64_t)(2 * sg.ca + 1) * p.part_rows + pr) * kAtPartRow;
+            const float* next = p.part + ((int64_t)2 * sg.ca * p.part_rows + pr) * kAtPartRow + state;
+            float M = -INFINITY, L = 0.0f;
+            float o[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+#pragma unroll 2
+            for (int c = sg.ca; c <= sg.cb; ++c) {
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(st));
+              float4 x[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[i] = __ldcg(reinterpret_cast<const float4*>(st + 4) + (lane & 7) + 8 * i);
+              st = next;
+              next += state;
+              const float Mn = fmaxf(M, ml.x), sub = Mn == -INFINITY ? 0.0f : Mn;
+              const float f = fast_exp2(M - sub), g = fast_exp2(ml.x - sub);
+              M = Mn;
+              L = L * f + ml.y * g;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[4 * i] = o[4 * i] * f + x[i].x * g;
+                o[4 * i + 1] = o[4 * i + 1] * f + x[i].y * g;
+                o[4 * i + 2] = o[4 * i + 2] * f + x[i].z * g;
+                o[4 * i + 3] = o[4 * i + 3] * f + x[i].w * g;
               }
             }
             const float inv = L > 0.0f ? 1.0f / L : 0.0f;
             const int tk = pr / G;
             const int64_t row = (int64_t)(pl.first[sg.u.b] + sg.u.tok0 + tk) * p.c.Hq + sg.u.h * G + (pr - tk * G);
-            uint32_t y0, y1;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y0) : "f"(o.y * inv), "f"(o.x * inv));
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y1) : "f"(o.w * inv), "f"(o.z * inv));
-            reinterpret_cast<uint2*>(p.c.out + row * kDim)[lane] = make_uint2(y0, y1);
-            if (lane == 0 && p.c.lse) p.c.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t y0, y1;
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y0) : "f"(o[4 * i + 1] * inv), "f"(o[4 * i] * inv));
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y1) : "f"(o[4 * i + 3] * inv), "f"(o[4 * i + 2] * inv));
+              reinterpret_cast<uint2*>(p.c.out + row * kDim)[(lane & 7) + 8 * i] = make_uint2(y0, y1);
+            }
+            if ((lane & 7) == 0 && p.c.lse) p.c.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
           }
         }
         named_sync(1, 256);  // last_flag is read before the next unit sets it
@@ -490,7 +523,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
       uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
       AtWalk w = at_start(pl);
       AtSegment sg;
-      uint32_t it = 0, nseg = 0;
+      uint32_t it = 0, nseg = 0, tails = 0;
       bool bad = false;
       while (at_next(pl, p, w, sg)) {
         if (!is_v) {  // Q: the live rows of both tiles
@@ -514,6 +547,33 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
         for (int j = sg.t0; j < sg.t1; ++j, ++it) {
           const int stage = it % kAtStages;
           const uint32_t dst = ring + stage * kTileBytes;
+          const uint32_t par = ((it / kAtStages) & 1) ^ 1;
+          if (p.box) {
+            const int seen = sg.u.kv_end - j * 128;  // rows of the tile that some row sees
+            const int pieces = seen <= 0 ? 0 : ((seen < 128 ? seen : 128) + p.box - 1) / p.box;
+            uint32_t row = 0;
+            if (lt < pieces) row = p.c.geo.row32(sg.u.b, sg.u.h, j * 128 + lt * p.box, bad);
+            mbar_wait_or_give_up(&empty[stage], par, &gave_up);
+            const bool zeros = is_v && seen < 128;
+            uint64_t* bar = zeros ? &v_tail : &full[stage];
+            if (lt == 0) mbar_arrive_expect_tx(bar, (uint32_t)(pieces * p.box * 2 * kDim));
+            if (lt < 32) {
+              __syncwarp();
+              if (lt < pieces) {
+                const void* map = is_v ? &v_map : &k_map;
+                tma_load_2d(dst + lt * p.box * 128, map, 0, (int)row, bar);
+                tma_load_2d(dst + kTileHalf + lt * p.box * 128, map, 64, (int)row, bar);
+              }
+            }
+            if (zeros) {
+              mbar_wait_or_give_up(&v_tail, tails++ & 1, &gave_up);
+              for (int r = (seen < 0 ? 0 : seen) + lr; r < 128; r += 4)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + tile_piece(r, lc)), "r"(0) : "memory");
+              fence_async_smem();
+            }
+            if (lt != 0 || zeros) mbar_arrive(&full[stage]);
+            continue;
+          }
           const int tb = j * 128 + lr;
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {  // rows 64 hf + lr + 4 i
@@ -523,7 +583,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
               const int tk = tb + 64 * hf + 4 * i;
               row[i] = tk < sg.u.kv_end ? p.c.geo.row32(sg.u.b, sg.u.h, tk, bad) : 0u;
             }
-            if (hf == 0) mbar_wait_or_give_up(&empty[stage], ((it / kAtStages) & 1) ^ 1, &gave_up);
+            if (hf == 0) mbar_wait_or_give_up(&empty[stage], par, &gave_up);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               cp_async16_or_zero(dst + piece[i & 1] + 8192 * hf + 1024 * (i >> 1), rows_of + (int64_t)row[i] * kDim,
@@ -547,7 +607,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
         };
         auto k_wait = [&]() {
           mbar_wait_or_give_up(&k_full[ik % kAtStages], (ik / kAtStages) & 1, &gave_up);
-          fence_async_smem();
+          if (!p.box) fence_async_smem();
         };
         auto k_next = [&]() { mma_commit(&k_empty[ik++ % kAtStages]); };
         auto outputs = [&](int t, bool acc) {
@@ -560,6 +620,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
           const bool two = sg.u.ntok > p.TQ;
           const int n = sg.t1 - sg.t0, ahead = two ? 1 : 2;  // K tiles whose scores are under way
           mbar_wait_or_give_up(&q_full, nseg & 1, &gave_up);
+          fence_async_smem();
           ++nseg;
           for (int j = 0; j < ahead && j < n; ++j) {
             k_wait();
@@ -570,7 +631,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) chunk_attend_kernel(const AtPar
           }
           for (int j = 0; j < n; ++j) {
             mbar_wait_or_give_up(&v_full[iv % kAtStages], (iv / kAtStages) & 1, &gave_up);
-            fence_async_smem();
+            if (!p.box) fence_async_smem();
             const bool more = j + ahead < n;
             if (two) {
               if (more) k_wait();

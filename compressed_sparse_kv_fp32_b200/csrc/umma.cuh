@@ -138,6 +138,15 @@ __device__ __forceinline__ void mbar_wait_or_give_up(uint64_t* bar, uint32_t par
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
+// One box of a two-dimensional tensor map (64 columns at x, a multiple of 64, and the
+// map's box of rows at y) to shared memory, in the map's 128-byte swizzle; its bytes are
+// counted on the barrier.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
 // The barrier is arrived at once when every cp.async this thread issued before has landed
 // (the arrival counts as one of those the barrier expects).  Whoever waits for it runs
 // fence_async_smem() before the tensor core reads what landed.

@@ -450,7 +450,8 @@ int adamas_rope_append(const adamas_rope_args *args, adamas_stream_t stream);
  * Scores, softmax statistics and output sums are fp32; the probabilities are
  * rounded to bf16 for their product with V (V is bf16 as well), the sum they are
  * divided by is not.  V rows are finite: a tile's masked products are 0 * V.
- * The same inputs give the same bits on every run.
+ * The same inputs give the same bits on every run.  K and V are at most 2^31 - 1
+ * rows each (half a terabyte).
  */
 typedef struct adamas_chunk_args {
     const void *q;
