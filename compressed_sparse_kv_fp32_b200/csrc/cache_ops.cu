@@ -79,13 +79,14 @@ static int attend_device(int* sms) {
   return ADAMAS_OK;
 }
 
-// A tensor map over the rows of K or V: 128 columns in two boxes of 64 (128 bytes), `box`
-// rows each.  The encoder is a driver call, reached through the runtime.
+// Tensor maps of bf16 arrays for copies of 64 columns (128 bytes, the swizzle's width).  The
+// encoder is a driver call, reached through the runtime.
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-static int rows_map(const void* base, int64_t rows, int box, CUtensorMap* map) {
+static int tile_map(const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                    const cuuint32_t* boxes, CUtensorMap* map) {
   static std::atomic<EncodeTiledFn> known{nullptr};
   EncodeTiledFn fn = known.load(std::memory_order_acquire);
   if (!fn) {
@@ -97,12 +98,26 @@ static int rows_map(const void* base, int64_t rows, int box, CUtensorMap* map) {
     fn = reinterpret_cast<EncodeTiledFn>(f);
     known.store(fn, std::memory_order_release);
   }
-  const cuuint64_t dims[2] = {(cuuint64_t)kDim, (cuuint64_t)rows}, strides[1] = {2 * kDim};
-  const cuuint32_t boxes[2] = {64, (cuuint32_t)box}, steps[2] = {1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, steps,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint32_t steps[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides,
+                        boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? ADAMAS_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
+// The rows of K or V, `box` of them a copy.
+static int rows_map(const void* base, int64_t rows, int box, CUtensorMap* map) {
+  const cuuint64_t dims[2] = {(cuuint64_t)kDim, (cuuint64_t)rows}, strides[1] = {2 * kDim};
+  const cuuint32_t boxes[2] = {64, (cuuint32_t)box};
+  return tile_map(base, 2, dims, strides, boxes, map);
+}
+
+// The queries [T][Hq][128] for copies of 64 columns, G heads and TQ tokens.
+static int query_map(const void* q, int T, int Hq, int G, int TQ, CUtensorMap* map) {
+  const cuuint64_t dims[3] = {(cuuint64_t)kDim, (cuuint64_t)Hq, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {2 * kDim, (cuuint64_t)Hq * 2 * kDim};
+  const cuuint32_t boxes[3] = {64, (cuuint32_t)G, (cuuint32_t)TQ};
+  return tile_map(q, 3, dims, strides, boxes, map);
 }
 
 // Rows of one tensor-map copy of a 128-row tile: all of them, or the largest power of two
@@ -230,7 +245,8 @@ int adamas_chunk_attend(const adamas_chunk_args* args, adamas_stream_t stream) {
   ap.TQ = 128 / p.G;
   const int64_t rows = a.block_table ? a.n_pages * p.Hkv * a.page_size : (int64_t)a.B * p.Hkv * p.geo.Nmax;
   if (rows > INT32_MAX) return ADAMAS_ERR_UNSUPPORTED;
-  CUtensorMap k_map = {}, v_map = {};
+  CUtensorMap q_map = {}, k_map = {}, v_map = {};
+  if ((rc = query_map(a.q, a.T, a.Hq, p.G, ap.TQ, &q_map)) != ADAMAS_OK) return rc;
   ap.box = rows > 0 ? rows_box(p.geo, a.page_size) : 0;
   if (ap.box && ((rc = rows_map(a.K, rows, ap.box, &k_map)) != ADAMAS_OK ||
                  (rc = rows_map(a.V, rows, ap.box, &v_map)) != ADAMAS_OK))
@@ -238,8 +254,8 @@ int adamas_chunk_attend(const adamas_chunk_args* args, adamas_stream_t stream) {
   // no more blocks than K/V tiles of all units
   const int64_t units = (int64_t)p.Hkv * ((a.T + 2 * ap.TQ - 1) / (2 * ap.TQ) + p.B);
   const int64_t tiles = units * ((p.geo.Nmax + 127) / 128 + 1);
-  chunk_attend_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kAtThreads, kAtSmem, (cudaStream_t)stream>>>(ap, k_map,
-                                                                                                            v_map);
+  chunk_attend_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kAtThreads, kAtSmem, (cudaStream_t)stream>>>(
+      ap, q_map, k_map, v_map);
   return launched();
 }
 

@@ -21,12 +21,12 @@
 // one row tile (decode) takes its K/V tiles in turn as tile 0 and tile 1 -- the second
 // copy of S and O would idle otherwise -- and merges the two states at its end.
 //
-// Work split.  Sequences with several units (prompts) fill whole waves of the grid,
-// heads that fit in L2 together next to each other and the longest units first, so that
-// the blocks of a wave read the same K and V tiles at about the same time.  What is left
-// over, and every sequence with a single unit (decode), is one line of K/V tiles cut
-// into equal shares, one per block: a unit cut by a share's end leaves partial states
-// in the workspace, and the block that arrives last merges them in the units' order.
+// Work split.  All units make one line of K/V tiles that is cut into equal shares, one per
+// block, so that every block does the same work whatever the lengths: a unit cut by a
+// share's end leaves partial states in the workspace, and the block that arrives last
+// merges them in the blocks' order.  Sequences with several units (prompts) come first,
+// heads whose K and V fit in L2 together next to each other, so that the blocks at work
+// on them at one time read K and V from L2.
 #pragma once
 
 #include <cuda.h>
@@ -42,16 +42,21 @@ constexpr int kAtMaxGrid = 160;
 constexpr int kAtPartRow = 132;             // m, l, -, -, o[128]
 constexpr int64_t kAtL2Bytes = 48ll << 20;  // K and V of heads that go through a wave together
 
+// Where a block's share of the line begins, and how it goes on from there.
+struct AtWalk {
+  long long x, x1;  // K/V tiles [x, x1) of the line are still to do
+  int b, group, q, h;  // sequence, group of heads, unit of the chunk, head in the group: the unit of tile x
+  int t;               // tile x's number in the unit
+};
+
 // Plan of a launch, made by every block for itself (the lengths are on the device).
 struct AtPlan {
-  int mpre[kMaxBatch + 1];            // units of the sequences with several, before each
-  long long spre[kMaxBatch + 1];      // tiles of the sequences with one unit per head, before each
-  long long lpre[kAtMaxGrid + 1];            // tiles of the left-over units, before each
-  int first[kMaxBatch];               // the sequence's rows
+  long long tiles[kMaxBatch + 1];  // K/V tiles of the line before each sequence
+  int first[kMaxBatch];            // the sequence's rows
   int n[kMaxBatch];
   int len[kMaxBatch];
-  long long W, Wl;   // tiles of the line, of its left-over units
-  int waves, left, shares;
+  int shares;
+  AtWalk start;
 };
 
 constexpr size_t kAtSmem = 2 * kTileBytes + 2 * kAtStages * kTileBytes + 1024;
@@ -79,11 +84,6 @@ struct AtSegment {
   int slot, ca, cb;  // partial state's place; blocks that share the unit
 };
 
-struct AtWalk {
-  int wave = 0;
-  long long x, x1;
-};
-
 __device__ __forceinline__ AtUnit at_unit(const AtPlan& pl, const AtParams& p, int b, int h, int qi) {
   AtUnit u;
   const int tu = 2 * p.TQ;
@@ -98,75 +98,51 @@ __device__ __forceinline__ AtUnit at_unit(const AtPlan& pl, const AtParams& p, i
   return u;
 }
 
-// unit number u of the sequences with several: by groups of heads whose K and V fit in
-// L2, then from the chunk's last tokens (the longest) to its first
-__device__ __forceinline__ AtUnit at_multi_unit(const AtPlan& pl, const AtParams& p, int u) {
-  int lo = 0, hi = p.c.B;  // mpre[lo] <= u < mpre[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pl.mpre[mid] <= u) lo = mid;
-    else hi = mid;
-  }
-  const int Hkv = p.c.Hkv, local = u - pl.mpre[lo], nu = (pl.mpre[hi] - pl.mpre[lo]) / Hkv;
-  int64_t hg = kAtL2Bytes / ((int64_t)(pl.len[lo] > 0 ? pl.len[lo] : 1) * 4 * kDim);
-  hg = hg < 1 ? 1 : (hg > Hkv ? Hkv : hg);
-  const int per = nu * (int)hg, gi = local / per, rem = local - gi * per;
-  const int hc = Hkv - gi * (int)hg < (int)hg ? Hkv - gi * (int)hg : (int)hg;
-  const int q = rem / hc;
-  return at_unit(pl, p, lo, gi * (int)hg + (rem - q * hc), nu - 1 - q);
+// Units of a sequence per head, and the heads of a group: as many as have their K and V
+// in L2 together.
+__device__ __forceinline__ int at_units(const AtPlan& pl, const AtParams& p, int b) {
+  return (pl.n[b] + 2 * p.TQ - 1) / (2 * p.TQ);
+}
+__device__ __forceinline__ int at_group(const AtPlan& pl, const AtParams& p, int b) {
+  const uint32_t fit = (uint32_t)(kAtL2Bytes / (4 * kDim)) / (uint32_t)(pl.len[b] > 0 ? pl.len[b] : 1);
+  return fit < 1 ? 1 : (fit > (uint32_t)p.c.Hkv ? p.c.Hkv : (int)fit);
 }
 
+// The next piece of the block's share.  The line's order: sequences, groups of heads,
+// units from the chunk's last tokens to its first, heads of the group.
 __device__ __forceinline__ bool at_next(const AtPlan& pl, const AtParams& p, AtWalk& w, AtSegment& s) {
-  const int n = gridDim.x, c = blockIdx.x;
-  if (w.wave < pl.waves) {
-    s.u = at_multi_unit(pl, p, w.wave * n + ((w.wave & 1) ? n - 1 - c : c));
-    ++w.wave;
-    s.t0 = 0;
-    s.t1 = s.u.tiles;
-    s.part = false;
-    return true;
-  }
   if (w.x >= w.x1) return false;
-  long long f0, f1;
-  if (w.x < pl.Wl) {
-    int lo = 0, hi = pl.left;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pl.lpre[mid] <= w.x) lo = mid;
-      else hi = mid;
-    }
-    s.u = at_multi_unit(pl, p, pl.waves * n + lo);
-    f0 = pl.lpre[lo];
-    f1 = pl.lpre[lo + 1];
-  } else {
-    const long long y = w.x - pl.Wl;
-    int lo = 0, hi = p.c.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pl.spre[mid] <= y) lo = mid;
-      else hi = mid;
-    }
-    const int tiles = (int)((pl.spre[hi] - pl.spre[lo]) / p.c.Hkv);
-    const int h = (int)((y - pl.spre[lo]) / tiles);
-    s.u = at_unit(pl, p, lo, h, 0);
-    f0 = pl.Wl + pl.spre[lo] + (long long)h * tiles;
-    f1 = f0 + tiles;
-  }
-  s.t0 = (int)(w.x - f0);
-  const long long e = w.x1 < f1 ? w.x1 : f1;
+  const int hg = at_group(pl, p, w.b);
+  s.u = at_unit(pl, p, w.b, w.group * hg + w.h, w.q);
+  const long long f0 = w.x - w.t, f1 = f0 + s.u.tiles, e = w.x1 < f1 ? w.x1 : f1;
+  s.t0 = w.t;
   s.t1 = (int)(e - f0);
-  w.x = e;
-  s.part = s.t0 != 0 || e != f1;
-  s.slot = 2 * c + (s.t0 == 0 ? 1 : 0);
+  s.part = w.t != 0 || e != f1;
+  s.slot = 2 * (int)blockIdx.x + (w.t == 0 ? 1 : 0);
   if (s.part) {  // the blocks whose shares hold the unit's first and last tile
-    s.ca = (int)(((f0 + 1) * pl.shares - 1) / pl.W);
-    s.cb = (int)((f1 * pl.shares - 1) / pl.W);
+    const long long W = pl.tiles[p.c.B];
+    s.ca = (int)(((f0 + 1) * pl.shares - 1) / W);
+    s.cb = (int)((f1 * pl.shares - 1) / W);
+  }
+  w.x = e;
+  w.t = 0;
+  if (++w.h == (p.c.Hkv - w.group * hg < hg ? p.c.Hkv - w.group * hg : hg)) {
+    w.h = 0;
+    if (--w.q < 0) {
+      ++w.group;
+      if (w.group * hg >= p.c.Hkv && w.x < w.x1) {
+        w.group = 0;
+        do ++w.b;
+        while (pl.n[w.b] == 0);  // there are tiles left, so a sequence with rows follows
+      }
+      if (w.x < w.x1) w.q = at_units(pl, p, w.b) - 1;
+    }
   }
   return true;
 }
 
 __device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, int tid) {
-  const int B = p.c.B, tu = 2 * p.TQ;
+  const int B = p.c.B, lane = tid & 31, warp = tid >> 5;
   bool bad_cu = false, bad_len = false;
   for (int b = tid; b < B; b += kAtThreads) {
     int first, n;
@@ -178,77 +154,78 @@ __device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, int 
   if (bad_cu) atomicOr(p.c.err, kErrOffsets);
   if (bad_len) atomicOr(p.c.err, kErrSeqLen);
   __syncthreads();
-  if (tid < 32) {
-    int mu = 0;
-    long long st = 0;
-    for (int b0 = 0; b0 < B; b0 += 32) {
-      const int b = b0 + tid;
-      int m = 0;
-      long long s = 0;
-      if (b < B && pl.n[b] > 0) {
-        const int nu = (pl.n[b] + tu - 1) / tu;
-        if (nu > 1) m = nu * p.c.Hkv;
-        else s = (long long)p.c.Hkv * (pl.len[b] == 0 ? 1 : (pl.len[b] + 127) / 128);
-      }
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int mm = __shfl_up_sync(0xffffffffu, m, d);
-        const long long ss = __shfl_up_sync(0xffffffffu, s, d);
-        if (tid >= d) {
-          m += mm;
-          s += ss;
-        }
-      }
-      if (b < B) {
-        pl.mpre[b + 1] = mu + m;
-        pl.spre[b + 1] = st + s;
-      }
-      mu += __shfl_sync(0xffffffffu, m, 31);
-      st += __shfl_sync(0xffffffffu, s, 31);
-    }
-    if (tid == 0) {
-      pl.mpre[0] = 0;
-      pl.spre[0] = 0;
-      pl.waves = mu / (int)gridDim.x;
-      pl.left = mu - pl.waves * (int)gridDim.x;
-    }
-  }
-  __syncthreads();
-  if (tid < pl.left) pl.lpre[tid + 1] = at_multi_unit(pl, p, pl.waves * (int)gridDim.x + tid).tiles;
-  __syncthreads();
-  if (tid < 32) {
+  for (int b = warp; b < B; b += kAtThreads / 32) {
+    const int nu = at_units(pl, p, b);
     long long sum = 0;
-    for (int i0 = 1; i0 <= pl.left; i0 += 32) {
-      long long v = i0 + tid <= pl.left ? pl.lpre[i0 + tid] : 0;
+    for (int q = lane; q < nu; q += 32) sum += at_unit(pl, p, b, 0, q).tiles;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) pl.tiles[b + 1] = sum * p.c.Hkv;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long all = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      long long s = b0 + lane < B ? pl.tiles[b0 + lane + 1] : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, d);
-        if (tid >= d) v += u;
+        const long long u = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += u;
       }
-      v += sum;
-      if (i0 + tid <= pl.left) pl.lpre[i0 + tid] = v;
-      sum = __shfl_sync(0xffffffffu, v, 31);
+      s += all;
+      if (b0 + lane < B) pl.tiles[b0 + lane + 1] = s;
+      all = __shfl_sync(0xffffffffu, s, 31);
     }
-    if (tid == 0) {
-      pl.lpre[0] = 0;
-      pl.Wl = sum;
-      pl.W = sum + pl.spre[B];
-      pl.shares = pl.W < (long long)gridDim.x ? (int)pl.W : (int)gridDim.x;  // no share is empty
+    if (lane == 0) pl.tiles[0] = 0;
+    __syncwarp();
+    const int shares = all < (long long)gridDim.x ? (int)all : (int)gridDim.x;  // no share is empty
+    AtWalk w = {0, 0, 0, 0, 0, 0, 0};
+    if ((int)blockIdx.x < shares) {
+      w.x = all * blockIdx.x / shares;
+      w.x1 = all * (blockIdx.x + 1) / shares;
+      int lo = 0, hi = B;  // tiles[lo] <= x < tiles[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pl.tiles[mid] <= w.x) lo = mid;
+        else hi = mid;
+      }
+      w.b = lo;
+      const int hg = at_group(pl, p, lo), nu = at_units(pl, p, lo);
+      const long long per_head = (pl.tiles[lo + 1] - pl.tiles[lo]) / p.c.Hkv, y0 = w.x - pl.tiles[lo];
+      w.group = (int)(y0 / (per_head * hg));
+      long long y = y0 - w.group * hg * per_head, before = 0;
+      const int hc = p.c.Hkv - w.group * hg < hg ? p.c.Hkv - w.group * hg : hg;
+      for (int k0 = 0; k0 < nu; k0 += 32) {
+        const int tiles = k0 + lane < nu ? at_unit(pl, p, lo, 0, nu - 1 - k0 - lane).tiles : 0;
+        long long s = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long u = __shfl_up_sync(0xffffffffu, s, d);
+          if (lane >= d) s += u;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, y < hc * (before + s));
+        if (here) {
+          const int l = __ffs(here) - 1;
+          const int tl = __shfl_sync(0xffffffffu, tiles, l);
+          y -= hc * (before + __shfl_sync(0xffffffffu, s, l) - tl);
+          w.q = nu - 1 - k0 - l;
+          w.h = (int)(y / tl);
+          w.t = (int)(y - (long long)w.h * tl);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, s, 31);
+      }
+    }
+    if (lane == 0) {
+      pl.shares = shares;
+      pl.start = w;
     }
   }
   __syncthreads();
-}
-
-__device__ __forceinline__ AtWalk at_start(const AtPlan& pl) {
-  AtWalk w;
-  const int c = blockIdx.x;
-  w.x = c < pl.shares ? pl.W * c / pl.shares : 0;
-  w.x1 = c < pl.shares ? pl.W * (c + 1) / pl.shares : 0;
-  return w;
 }
 
 __global__ void __launch_bounds__(kAtThreads, 1)
-    chunk_attend_kernel(const AtParams p, const __grid_constant__ CUtensorMap k_map,
+    chunk_attend_kernel(const AtParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                         const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ AtPlan pl;
@@ -261,7 +238,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   const uint32_t q_tile = base, k_ring = base + 2 * kTileBytes, v_ring = k_ring + kAtStages * kTileBytes;
 
   if (tid == 0) {
-    mbar_init(&q_full, 64);
+    mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
@@ -287,13 +264,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax and epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int t = warp >> 2;                      // tile
     const int r = (warp & 3) * 32 + lane;         // row of the tile
     const uint32_t quad = (uint32_t)(warp & 3) << 21;  // 32 lanes, in the address's upper half
     const uint32_t S = tmem + quad + 128 * t, O = tmem + quad + 256 + 128 * t;
     const int G = p.c.G, rt = r / G, rg = r - rt * G;  // the row's token in the tile, its head in the group
-    AtWalk w = at_start(pl);
+    AtWalk w = pl.start;
     AtSegment sg;
     uint32_t s_par = 0, o_par = 0;
     while (at_next(pl, p, w, sg)) {
@@ -313,29 +290,25 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           s_par ^= 1;
           if (warp_live) {
             tmem_fence_after();
-            float s[128];
-            {
-              uint32_t x[4][32];
-              tmem_ld32(S, x[0]);
-              tmem_ld32(S + 32, x[1]);
-              tmem_ld32(S + 64, x[2]);
-              tmem_ld32(S + 96, x[3]);
-              tmem_wait_ld();
+            uint32_t x[4][32];
+            tmem_ld32(S, x[0]);
+            tmem_ld32(S + 32, x[1]);
+            tmem_ld32(S + 64, x[2]);
+            tmem_ld32(S + 96, x[3]);
 #pragma unroll
-              for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(x[i >> 5][i & 31]);
-            }
-            if (j * 128 + 128 > vis_all) {
+            for (int c = 0; c < 4; ++c) tmem_wait_ld(x[c]);
+            if (j * 128 + 128 > vis_all) {  // some row does not see the whole tile
               const int seen = vis - j * 128;
 #pragma unroll
-              for (int i = 0; i < 128; ++i) s[i] = i < seen ? s[i] : -INFINITY;
+              for (int i = 0; i < 128; ++i) x[i >> 5][i & 31] = i < seen ? x[i >> 5][i & 31] : 0xFF800000u;
             }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 4; i < 128; i += 8) {
+            for (int i = 0; i < 128; i += 8)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(s[i + k], i + 4 + k < 128 ? s[i + 4 + k] : s[i + k]));
-            }
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScoreLog2;
+              for (int k = 0; k < 4; ++k)
+                mx[k] = max3(mx[k], __uint_as_float(x[i >> 5][(i & 31) + k]), __uint_as_float(x[i >> 5][(i & 31) + 4 + k]));
+            const float mt = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * kScoreLog2;
             const bool raise = mt > m + 8.0f;  // also when m is -inf and a score is not
             if (__any_sync(0xffffffffu, raise)) {
               const float mn = raise ? mt : m;
@@ -344,32 +317,39 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               l *= f;
               if (j > j0) {  // every product into O is done: S of this tile came after them
 #pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
-                  uint32_t x[32];
-                  tmem_ld32(O + c, x);
-                  tmem_wait_ld();
+                for (int c = 0; c < 128; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(O + c, o);
+                  tmem_wait_ld16(o);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                  tmem_st32(O + c, x);
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st16(O + c, o);
                 }
               }
             }
             const float sub = m == -INFINITY ? 0.0f : m;
-            float sum[4] = {0, 0, 0, 0};
+            const uint64_t scale2 = f2_pack(kScoreLog2, kScoreLog2), sub2 = f2_pack(-sub, -sub);
+            uint64_t sum[2] = {0, 0};  // two pairs of fp32 sums
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              uint32_t x[32];
+            for (int c = 0; c < 4; ++c) {
+              uint32_t y[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float a = fast_exp2(fmaf(s[64 * hf + 2 * i], kScoreLog2, -sub));
-                const float b = fast_exp2(fmaf(s[64 * hf + 2 * i + 1], kScoreLog2, -sub));
-                sum[i & 1] += a;
-                sum[2 + (i & 1)] += b;
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x[i]) : "f"(b), "f"(a));
+              for (int i = 0; i < 16; ++i) {
+                const uint64_t e = f2_fma(f2_pack(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), scale2, sub2);
+                float a, b;
+                f2_unpack(e, a, b);
+                a = fast_exp2(a);
+                b = fast_exp2(b);
+                sum[i & 1] = f2_add(sum[i & 1], f2_pack(a, b));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[i]) : "f"(b), "f"(a));
               }
-              tmem_st32(S + 32 * hf, x);
+              tmem_st16(S + 16 * c, y);  // over columns of S that were read
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            {
+              float a, b;
+              f2_unpack(f2_add(sum[0], sum[1]), a, b);
+              l += a + b;
+            }
             tmem_wait_st();
             tmem_fence_before();
           }
@@ -413,11 +393,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           for (int c = 0; c < 128; c += 32) {
             uint32_t x[32];
             tmem_ld32(O + c, x);
-            tmem_wait_ld();
+            tmem_wait_ld(x);
             if (merge) {
               uint32_t y[32];
               tmem_ld32(O + 128 + c, y);
-              tmem_wait_ld();
+              tmem_wait_ld(y);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 x[i] = __float_as_uint(__uint_as_float(x[i]) * fa + __uint_as_float(y[i]) * fb);
@@ -512,7 +492,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp < 12) {
       // ---------------------------------------------------------- copies
       const bool is_v = warp >= 10;
@@ -521,29 +501,21 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const uint16_t* rows_of = (is_v ? p.c.V : p.c.K) + lc * 8;
       const uint32_t ring = is_v ? v_ring : k_ring;
       uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
-      AtWalk w = at_start(pl);
+      AtWalk w = pl.start;
       AtSegment sg;
       uint32_t it = 0, nseg = 0, tails = 0;
       bool bad = false;
       while (at_next(pl, p, w, sg)) {
-        if (!is_v) {  // Q: the live rows of both tiles
+        if (!is_v && lt == 0) {  // Q: TQ tokens' heads of the group are TQ * G rows of a tile
           mbar_wait_or_give_up(&q_empty, (nseg & 1) ^ 1, &gave_up);
-          ++nseg;
-#pragma unroll 1
-          for (int t = 0; t < 2; ++t) {
-            int rows = (sg.u.ntok - t * p.TQ) * p.c.G;
-            if (rows > p.TQ * p.c.G) rows = p.TQ * p.c.G;
-            const uint16_t* q = p.c.q + (int64_t)(pl.first[sg.u.b] + sg.u.tok0 + t * p.TQ) * p.c.Hq * kDim +
-                                (int64_t)sg.u.h * p.c.G * kDim + lc * 8;
-#pragma unroll 1
-            for (int r = lr; r < rows; r += 4) {
-              const int tk = r / p.c.G;
-              cp_async16_or_zero(q_tile + t * kTileBytes + tile_piece(r, lc),
-                                 q + ((int64_t)tk * p.c.Hq + (r - tk * p.c.G)) * kDim, true);
-            }
+          const int nt = sg.u.ntok > p.TQ ? 2 : 1, tok = pl.first[sg.u.b] + sg.u.tok0;
+          mbar_arrive_expect_tx(&q_full, (uint32_t)(nt * p.TQ * p.c.G * 2 * kDim));
+          for (int t = 0; t < nt; ++t) {
+            tma_load_3d(q_tile + t * kTileBytes, &q_map, 0, sg.u.h * p.c.G, tok + t * p.TQ, &q_full);
+            tma_load_3d(q_tile + t * kTileBytes + kTileHalf, &q_map, 64, sg.u.h * p.c.G, tok + t * p.TQ, &q_full);
           }
-          cp_async_arrive(&q_full);
         }
+        ++nseg;
         for (int j = sg.t0; j < sg.t1; ++j, ++it) {
           const int stage = it % kAtStages;
           const uint32_t dst = ring + stage * kTileBytes;
@@ -575,19 +547,19 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             continue;
           }
           const int tb = j * 128 + lr;
+          mbar_wait_or_give_up(&empty[stage], par, &gave_up);
 #pragma unroll 1
-          for (int hf = 0; hf < 2; ++hf) {  // rows 64 hf + lr + 4 i
-            uint32_t row[16];
+          for (int i0 = 0; i0 < 128; i0 += 32) {  // rows i0 + lr + 4 i
+            uint32_t row[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int tk = tb + 64 * hf + 4 * i;
+            for (int i = 0; i < 8; ++i) {
+              const int tk = tb + i0 + 4 * i;
               row[i] = tk < sg.u.kv_end ? p.c.geo.row32(sg.u.b, sg.u.h, tk, bad) : 0u;
             }
-            if (hf == 0) mbar_wait_or_give_up(&empty[stage], par, &gave_up);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              cp_async16_or_zero(dst + piece[i & 1] + 8192 * hf + 1024 * (i >> 1), rows_of + (int64_t)row[i] * kDim,
-                                 tb + 64 * hf + 4 * i < sg.u.kv_end);
+            for (int i = 0; i < 8; ++i)
+              cp_async16_or_zero(dst + piece[i & 1] + 128 * i0 + 1024 * (i >> 1), rows_of + (int64_t)row[i] * kDim,
+                                 tb + i0 + 4 * i < sg.u.kv_end);
           }
           cp_async_arrive(&full[stage]);
         }
@@ -597,7 +569,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     } else if (warp == 12) {
       // ---------------------------------------------------------- products
       if (lane == 0) {
-        AtWalk w = at_start(pl);
+        AtWalk w = pl.start;
         AtSegment sg;
         uint32_t ik = 0, iv = 0, nseg = 0, p_par[2] = {0, 0};
         // K tile -> S of t for the row tiles of the unit (or its only one)
@@ -610,8 +582,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           if (!p.box) fence_async_smem();
         };
         auto k_next = [&]() { mma_commit(&k_empty[ik++ % kAtStages]); };
-        auto outputs = [&](int t, bool acc) {
-          mbar_wait_or_give_up(&p_full[t], p_par[t], &gave_up);
+        auto outputs = [&](int t, bool acc, bool known) {
+          if (!known) mbar_wait_or_give_up(&p_full[t], p_par[t], &gave_up);
           p_par[t] ^= 1;
           tmem_fence_after();
           mma_probs_rows(tmem + 256 + 128 * t, tmem + 128 * t, v_ring + (iv % kAtStages) * kTileBytes, acc);
@@ -620,7 +592,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           const bool two = sg.u.ntok > p.TQ;
           const int n = sg.t1 - sg.t0, ahead = two ? 1 : 2;  // K tiles whose scores are under way
           mbar_wait_or_give_up(&q_full, nseg & 1, &gave_up);
-          fence_async_smem();
           ++nseg;
           for (int j = 0; j < ahead && j < n; ++j) {
             k_wait();
@@ -630,32 +601,40 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             k_next();
           }
           for (int j = 0; j < n; ++j) {
-            mbar_wait_or_give_up(&v_full[iv % kAtStages], (iv / kAtStages) & 1, &gave_up);
-            if (!p.box) fence_async_smem();
+            // what the next products wait for, asked for at once: each answer takes some 150
+            // cycles, in which the tensor cores have nothing to do
             const bool more = j + ahead < n;
+            const bool v_in = mbar_try(&v_full[iv % kAtStages], (iv / kAtStages) & 1);
+            const bool k_in = two && more && mbar_try(&k_full[ik % kAtStages], (ik / kAtStages) & 1);
+            const bool p_in = mbar_try(&p_full[two ? 0 : j & 1], p_par[two ? 0 : j & 1]);
+            if (!v_in) mbar_wait_or_give_up(&v_full[iv % kAtStages], (iv / kAtStages) & 1, &gave_up);
+            if (!p.box) fence_async_smem();
             if (two) {
-              if (more) k_wait();
+              if (more && !k_in) k_wait();
+              else if (!p.box) fence_async_smem();
               for (int t = 0; t < 2; ++t) {
-                outputs(t, j > 0);
+                outputs(t, j > 0, t == 0 && p_in);
                 if (more) scores(t, t);
                 else mma_commit(&o_full[t]);
               }
               mma_commit(&v_empty[iv++ % kAtStages]);
               if (more) k_next();
+              if (j + ahead + 1 == n) mma_commit(&q_empty);  // Q was read for the last time
             } else {
               const int t = j & 1;
-              outputs(t, j > 1);
+              outputs(t, j > 1, p_in);
               mma_commit(&v_empty[iv++ % kAtStages]);
               if (more) {
                 k_wait();
                 scores(t, 0);
                 k_next();
+                if (j + ahead + 1 == n) mma_commit(&q_empty);
               } else {
                 mma_commit(&o_full[t]);
               }
             }
           }
-          mma_commit(&q_empty);
+          if (n <= ahead) mma_commit(&q_empty);
         }
         mma_commit(&all_done);
         mbar_wait_or_give_up(&all_done, 0, &gave_up);

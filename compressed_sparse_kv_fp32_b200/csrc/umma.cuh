@@ -2,7 +2,7 @@
 // bf16 product with fp32 accumulators, and bounded barrier waits.
 #pragma once
 
-#include "common.cuh"
+#include "encode.cuh"  // packed fp32 pairs
 
 namespace adamas {
 
@@ -16,7 +16,6 @@ __device__ __forceinline__ void tmem_free512(uint32_t tmem) {
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 consecutive 32-bit columns of the lane's row (the warp's quadrant is in addr).
@@ -29,6 +28,31 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
+}
+// Waits for the thread's loads; the registers pass through so that nothing uses them before.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -70,36 +94,46 @@ __device__ __forceinline__ uint64_t desc_cols(uint32_t addr) {
 constexpr uint32_t kMma128 = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24);
 constexpr uint32_t kMma128Bcols = kMma128 | (1u << 16);
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
 // The barrier is arrived at once when every product this thread issued before is done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                : "memory");
 }
 
-// S = A B^T of two 128 x 128 tiles in shared memory (8 steps of 16 along the rows).
+// S = A B^T of two 128 x 128 tiles in shared memory (8 steps of 16 along the rows).  One
+// asm block: the descriptors are formed next to their use and hold no registers between.
 __device__ __forceinline__ void mma_rows_rows(uint32_t d, uint32_t a, uint32_t b) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t off = (uint32_t)((k >> 2) * kTileHalf + (k & 3) * 32);
-    mma_ss(d, desc_rows(a + off), desc_rows(b + off), kMma128, k > 0);
-  }
+  const uint64_t da = desc_rows(a), db = desc_rows(b);
+  asm volatile(
+      "{\n .reg .b64 x, y;\n .reg .pred p, q;\n setp.ne.u32 p, 0, 0;\n setp.eq.u32 q, 0, 0;\n"
+      " add.s64 x, %1, 0;\n add.s64 y, %2, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n"
+      " add.s64 x, %1, 2;\n add.s64 y, %2, 2;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n"
+      " add.s64 x, %1, 4;\n add.s64 y, %2, 4;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n"
+      " add.s64 x, %1, 6;\n add.s64 y, %2, 6;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n"
+      " add.s64 x, %1, 1024;\n add.s64 y, %2, 1024;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n"
+      " add.s64 x, %1, 1026;\n add.s64 y, %2, 1026;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n"
+      " add.s64 x, %1, 1028;\n add.s64 y, %2, 1028;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n"
+      " add.s64 x, %1, 1030;\n add.s64 y, %2, 1030;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n"
+      "}" ::"r"(d),
+      "l"(da), "l"(db), "r"(kMma128)
+      : "memory");
 }
 // O (+)= P V: P bf16 in tensor memory (64 columns), V's rows in shared memory.
 __device__ __forceinline__ void mma_probs_rows(uint32_t d, uint32_t p, uint32_t v, bool acc) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k) mma_ts(d, p + 8 * k, desc_cols(v + 2048 * k), kMma128Bcols, acc || k > 0);
+  const uint64_t dv = desc_cols(v);
+  asm volatile(
+      "{\n .reg .b64 y;\n .reg .b32 a;\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.eq.u32 q, 0, 0;\n"
+      " add.u32 a, %1, 0;\n add.s64 y, %2, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, p;\n"
+      " add.u32 a, %1, 8;\n add.s64 y, %2, 128;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, q;\n"
+      " add.u32 a, %1, 16;\n add.s64 y, %2, 256;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, q;\n"
+      " add.u32 a, %1, 24;\n add.s64 y, %2, 384;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, q;\n"
+      " add.u32 a, %1, 32;\n add.s64 y, %2, 512;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, q;\n"
+      " add.u32 a, %1, 40;\n add.s64 y, %2, 640;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, q;\n"
+      " add.u32 a, %1, 48;\n add.s64 y, %2, 768;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, q;\n"
+      " add.u32 a, %1, 56;\n add.s64 y, %2, 896;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, q;\n"
+      "}" ::"r"(d),
+      "r"(p), "l"(dv), "r"(kMma128Bcols), "r"((uint32_t)acc)
+      : "memory");
 }
 
 // ---------------------------------------------------------------- barriers, copies
@@ -147,6 +181,13 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x
       "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
 }
+// The same from a three-dimensional map: 64 columns at x, its box of y and z.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
 // The barrier is arrived at once when every cp.async this thread issued before has landed
 // (the arrival counts as one of those the barrier expects).  Whoever waits for it runs
 // fence_async_smem() before the tensor core reads what landed.
@@ -157,6 +198,11 @@ __device__ __forceinline__ float fast_exp2(float x) {  // 2 ulp; 0 for -inf
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
