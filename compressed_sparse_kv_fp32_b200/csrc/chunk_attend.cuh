@@ -44,22 +44,25 @@ constexpr int64_t kAtL2Bytes = 48ll << 20;  // K and V of heads that go through 
 
 // Where a block's share of the line begins, and how it goes on from there.
 struct AtWalk {
-  long long x, x1;  // K/V tiles [x, x1) of the line are still to do
-  int b, group, q, h;  // sequence, group of heads, unit of the chunk, head in the group: the unit of tile x
-  int t;               // tile x's number in the unit
+  long long x, x1;  // [x, x1) of the line is still to do
+  int b, group, q, h;  // sequence, group of heads, unit of the chunk, head in the group: the unit at x
+  int t;               // x's place in the unit
 };
 
-// Plan of a launch, made by every block for itself (the lengths are on the device).
+// What a block keeps of the launch's plan, which it makes for itself (the lengths are on
+// the device).
 struct AtPlan {
-  long long tiles[kMaxBatch + 1];  // K/V tiles of the line before each sequence
-  int first[kMaxBatch];            // the sequence's rows
-  int n[kMaxBatch];
-  int len[kMaxBatch];
+  long long W;  // length of the line
   int shares;
   AtWalk start;
 };
+constexpr int kAtUnitCost = 1;  // a unit's start and end cost about as much as one K/V tile
 
-constexpr size_t kAtSmem = 2 * kTileBytes + 2 * kAtStages * kTileBytes + 1024;
+// 32 rows of 128 bytes per softmax warp: rows pass through on their way out, so that a
+// store covers whole lines
+constexpr int kAtRowsOut = 32 * 128;
+constexpr size_t kAtSmem = 2 * kTileBytes + 2 * kAtStages * kTileBytes + 8 * kAtRowsOut + 1024;
+static_assert((kMaxBatch + 1) * sizeof(long long) <= 2 * kTileBytes, "the plan's table lies over the first tiles");
 
 struct AtParams {
   ChunkParams c;
@@ -71,7 +74,9 @@ struct AtParams {
 };
 
 struct AtUnit {
-  int b, h, tok0, ntok;  // sequence, kv head, first new token, new tokens
+  int b;                 // sequence
+  int h, ntok;           // kv head, new tokens
+  int row0;              // packed row of the first new token
   int pos0;              // slot of the first token (may be negative)
   int kv_end;            // slots that the last token sees
   int tiles;
@@ -84,14 +89,30 @@ struct AtSegment {
   int slot, ca, cb;  // partial state's place; blocks that share the unit
 };
 
-__device__ __forceinline__ AtUnit at_unit(const AtPlan& pl, const AtParams& p, int b, int h, int qi) {
+// A sequence of the batch: its rows and length.  (Read again for each unit: few lines, in
+// the first-level cache.)
+struct AtSeq {
+  int first, n, len;
+};
+__device__ __forceinline__ AtSeq at_seq(const AtParams& p, int b, bool& bad_cu, bool& bad_len) {
+  AtSeq s;
+  ragged_rows(p.c.cu_q, b, p.c.T, s.first, s.n, bad_cu);
+  s.len = (int)clamp_len(p.c.seq_lens[b], p.c.geo.Nmax, bad_len);
+  return s;
+}
+__device__ __forceinline__ AtSeq at_seq(const AtParams& p, int b) {
+  bool bad = false;
+  return at_seq(p, b, bad, bad);
+}
+
+__device__ __forceinline__ AtUnit at_unit(const AtParams& p, const AtSeq& sq, int b, int h, int qi) {
   AtUnit u;
-  const int tu = 2 * p.TQ;
+  const int tu = 2 * p.TQ, tok0 = qi * tu;
   u.b = b;
   u.h = h;
-  u.tok0 = qi * tu;
-  u.ntok = pl.n[b] - u.tok0 < tu ? pl.n[b] - u.tok0 : tu;
-  u.pos0 = pl.len[b] - pl.n[b] + u.tok0;
+  u.row0 = sq.first + tok0;
+  u.ntok = sq.n - tok0 < tu ? sq.n - tok0 : tu;
+  u.pos0 = sq.len - sq.n + tok0;
   const int end = u.pos0 + u.ntok;
   u.kv_end = end < 0 ? 0 : end;
   u.tiles = u.kv_end == 0 ? 1 : (u.kv_end + 127) / 128;
@@ -100,104 +121,108 @@ __device__ __forceinline__ AtUnit at_unit(const AtPlan& pl, const AtParams& p, i
 
 // Units of a sequence per head, and the heads of a group: as many as have their K and V
 // in L2 together.
-__device__ __forceinline__ int at_units(const AtPlan& pl, const AtParams& p, int b) {
-  return (pl.n[b] + 2 * p.TQ - 1) / (2 * p.TQ);
+__device__ __forceinline__ int at_units(const AtParams& p, const AtSeq& sq) {
+  return (sq.n + 2 * p.TQ - 1) / (2 * p.TQ);
 }
-__device__ __forceinline__ int at_group(const AtPlan& pl, const AtParams& p, int b) {
-  const uint32_t fit = (uint32_t)(kAtL2Bytes / (4 * kDim)) / (uint32_t)(pl.len[b] > 0 ? pl.len[b] : 1);
+__device__ __forceinline__ int at_group(const AtParams& p, const AtSeq& sq) {
+  const uint32_t fit = (uint32_t)(kAtL2Bytes / (4 * kDim)) / (uint32_t)(sq.len > 0 ? sq.len : 1);
   return fit < 1 ? 1 : (fit > (uint32_t)p.c.Hkv ? p.c.Hkv : (int)fit);
 }
 
 // The next piece of the block's share.  The line's order: sequences, groups of heads,
-// units from the chunk's last tokens to its first, heads of the group.
+// units from the chunk's last tokens to its first, heads of the group; a unit takes
+// kAtUnitCost places and one per K/V tile.
 __device__ __forceinline__ bool at_next(const AtPlan& pl, const AtParams& p, AtWalk& w, AtSegment& s) {
-  if (w.x >= w.x1) return false;
-  const int hg = at_group(pl, p, w.b);
-  s.u = at_unit(pl, p, w.b, w.group * hg + w.h, w.q);
-  const long long f0 = w.x - w.t, f1 = f0 + s.u.tiles, e = w.x1 < f1 ? w.x1 : f1;
-  s.t0 = w.t;
-  s.t1 = (int)(e - f0);
-  s.part = w.t != 0 || e != f1;
-  s.slot = 2 * (int)blockIdx.x + (w.t == 0 ? 1 : 0);
-  if (s.part) {  // the blocks whose shares hold the unit's first and last tile
-    const long long W = pl.tiles[p.c.B];
-    s.ca = (int)(((f0 + 1) * pl.shares - 1) / W);
-    s.cb = (int)((f1 * pl.shares - 1) / W);
-  }
-  w.x = e;
-  w.t = 0;
-  if (++w.h == (p.c.Hkv - w.group * hg < hg ? p.c.Hkv - w.group * hg : hg)) {
-    w.h = 0;
-    if (--w.q < 0) {
-      ++w.group;
-      if (w.group * hg >= p.c.Hkv && w.x < w.x1) {
-        w.group = 0;
-        do ++w.b;
-        while (pl.n[w.b] == 0);  // there are tiles left, so a sequence with rows follows
-      }
-      if (w.x < w.x1) w.q = at_units(pl, p, w.b) - 1;
+  while (w.x < w.x1) {
+    const AtSeq sq = at_seq(p, w.b);
+    const int hg = at_group(p, sq);
+    s.u = at_unit(p, sq, w.b, w.group * hg + w.h, w.q);
+    const long long f0 = w.x - w.t, f1 = f0 + kAtUnitCost + s.u.tiles, e = w.x1 < f1 ? w.x1 : f1;
+    s.t0 = w.t > kAtUnitCost ? w.t - kAtUnitCost : 0;
+    s.t1 = (int)(e - f0) - kAtUnitCost;
+    s.part = s.t0 != 0 || e != f1;
+    s.slot = 2 * (int)blockIdx.x + (s.t0 == 0 ? 1 : 0);
+    if (s.part) {  // the blocks whose shares hold the unit's first and last tile
+      s.ca = (int)(((f0 + kAtUnitCost + 1) * pl.shares - 1) / pl.W);
+      s.cb = (int)((f1 * pl.shares - 1) / pl.W);
     }
+    w.x = e;
+    w.t = 0;
+    if (e == f1 && w.x < w.x1 && ++w.h == (p.c.Hkv - w.group * hg < hg ? p.c.Hkv - w.group * hg : hg)) {
+      w.h = 0;
+      if (--w.q < 0) {
+        ++w.group;
+        AtSeq nx = sq;
+        if (w.group * hg >= p.c.Hkv) {
+          w.group = 0;
+          do nx = at_seq(p, ++w.b);  // the line goes on, so a sequence with rows follows
+          while (nx.n == 0);
+        }
+        w.q = at_units(p, nx) - 1;
+      }
+    }
+    if (s.t1 > s.t0) return true;  // else the share ends before the unit's first tile
   }
-  return true;
+  return false;
 }
 
-__device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, int tid) {
+// tab: kMaxBatch + 1 numbers of shared memory, free again afterwards.
+__device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, long long* tab, int tid) {
   const int B = p.c.B, lane = tid & 31, warp = tid >> 5;
-  bool bad_cu = false, bad_len = false;
-  for (int b = tid; b < B; b += kAtThreads) {
-    int first, n;
-    ragged_rows(p.c.cu_q, b, p.c.T, first, n, bad_cu);
-    pl.first[b] = first;
-    pl.n[b] = n;
-    pl.len[b] = (int)clamp_len(p.c.seq_lens[b], p.c.geo.Nmax, bad_len);
-  }
-  if (bad_cu) atomicOr(p.c.err, kErrOffsets);
-  if (bad_len) atomicOr(p.c.err, kErrSeqLen);
-  __syncthreads();
   for (int b = warp; b < B; b += kAtThreads / 32) {
-    const int nu = at_units(pl, p, b);
+    bool bad_cu = false, bad_len = false;
+    const AtSeq sq = at_seq(p, b, bad_cu, bad_len);
+    if (lane == 0 && bad_cu) atomicOr(p.c.err, kErrOffsets);
+    if (lane == 0 && bad_len) atomicOr(p.c.err, kErrSeqLen);
+    const int nu = at_units(p, sq);
     long long sum = 0;
-    for (int q = lane; q < nu; q += 32) sum += at_unit(pl, p, b, 0, q).tiles;
+    for (int q = lane; q < nu; q += 32) sum += at_unit(p, sq, b, 0, q).tiles + kAtUnitCost;
+    if (nu > 1) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) pl.tiles[b + 1] = sum * p.c.Hkv;
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    }
+    if (lane == 0) tab[b + 1] = sum * p.c.Hkv;
   }
   __syncthreads();
   if (warp == 0) {
     long long all = 0;
     for (int b0 = 0; b0 < B; b0 += 32) {
-      long long s = b0 + lane < B ? pl.tiles[b0 + lane + 1] : 0;
+      long long s = b0 + lane < B ? tab[b0 + lane + 1] : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const long long u = __shfl_up_sync(0xffffffffu, s, d);
         if (lane >= d) s += u;
       }
       s += all;
-      if (b0 + lane < B) pl.tiles[b0 + lane + 1] = s;
+      if (b0 + lane < B) tab[b0 + lane + 1] = s;
       all = __shfl_sync(0xffffffffu, s, 31);
     }
-    if (lane == 0) pl.tiles[0] = 0;
+    if (lane == 0) tab[0] = 0;
     __syncwarp();
-    const int shares = all < (long long)gridDim.x ? (int)all : (int)gridDim.x;  // no share is empty
+    // a share is a unit's start and a tile at least
+    const long long most = all / (kAtUnitCost + 1);
+    const int shares = most < (long long)gridDim.x ? (int)most : (int)gridDim.x;
     AtWalk w = {0, 0, 0, 0, 0, 0, 0};
     if ((int)blockIdx.x < shares) {
-      w.x = all * blockIdx.x / shares;
-      w.x1 = all * (blockIdx.x + 1) / shares;
-      int lo = 0, hi = B;  // tiles[lo] <= x < tiles[hi]
+      const bool narrow = all < (1ll << 31) / kAtMaxGrid;
+      w.x = narrow ? (uint32_t)all * blockIdx.x / (uint32_t)shares : all * blockIdx.x / shares;
+      w.x1 = narrow ? (uint32_t)all * (blockIdx.x + 1) / (uint32_t)shares : all * (blockIdx.x + 1) / shares;
+      int lo = 0, hi = B;  // tab[lo] <= x < tab[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (pl.tiles[mid] <= w.x) lo = mid;
+        if (tab[mid] <= w.x) lo = mid;
         else hi = mid;
       }
       w.b = lo;
-      const int hg = at_group(pl, p, lo), nu = at_units(pl, p, lo);
-      const long long per_head = (pl.tiles[lo + 1] - pl.tiles[lo]) / p.c.Hkv, y0 = w.x - pl.tiles[lo];
+      const AtSeq sq = at_seq(p, lo);
+      const int hg = at_group(p, sq), nu = at_units(p, sq);
+      const long long per_head = (tab[lo + 1] - tab[lo]) / p.c.Hkv, y0 = w.x - tab[lo];
       w.group = (int)(y0 / (per_head * hg));
       long long y = y0 - w.group * hg * per_head, before = 0;
       const int hc = p.c.Hkv - w.group * hg < hg ? p.c.Hkv - w.group * hg : hg;
       for (int k0 = 0; k0 < nu; k0 += 32) {
-        const int tiles = k0 + lane < nu ? at_unit(pl, p, lo, 0, nu - 1 - k0 - lane).tiles : 0;
-        long long s = tiles;
+        const int cost = k0 + lane < nu ? at_unit(p, sq, lo, 0, nu - 1 - k0 - lane).tiles + kAtUnitCost : 0;
+        long long s = cost;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const long long u = __shfl_up_sync(0xffffffffu, s, d);
@@ -206,22 +231,44 @@ __device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, int 
         const uint32_t here = __ballot_sync(0xffffffffu, y < hc * (before + s));
         if (here) {
           const int l = __ffs(here) - 1;
-          const int tl = __shfl_sync(0xffffffffu, tiles, l);
-          y -= hc * (before + __shfl_sync(0xffffffffu, s, l) - tl);
+          const int cl = __shfl_sync(0xffffffffu, cost, l);
+          y -= hc * (before + __shfl_sync(0xffffffffu, s, l) - cl);
           w.q = nu - 1 - k0 - l;
-          w.h = (int)(y / tl);
-          w.t = (int)(y - (long long)w.h * tl);
+          w.h = (int)(y / cl);
+          w.t = (int)(y - (long long)w.h * cl);
           break;
         }
         before += __shfl_sync(0xffffffffu, s, 31);
       }
     }
     if (lane == 0) {
+      pl.W = all;
       pl.shares = shares;
       pl.start = w;
     }
+    fence_async_smem();  // tensor-map copies write over the table next
   }
   __syncthreads();
+}
+
+// 32 rows of 128 bytes, one per lane in x, to their places (null: none): through shared
+// memory, so that each store instruction covers four whole lines.
+__device__ __forceinline__ void at_store_rows(uint32_t buf, const uint32_t (&x)[32], void* row, int lane) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((c ^ (lane & 7)) << 4)), "r"(x[4 * c]),
+                 "r"(x[4 * c + 1]), "r"(x[4 * c + 2]), "r"(x[4 * c + 3])
+                 : "memory");
+  __syncwarp();
+  const uint64_t mine = reinterpret_cast<uint64_t>(row);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3), c = lane & 7;
+    const uint64_t to = __shfl_sync(0xffffffffu, mine, r);
+    const uint4 v = lds128(buf + r * 128 + ((c ^ (r & 7)) << 4));
+    if (to) *reinterpret_cast<uint4*>(to + 16 * c) = v;
+  }
+  __syncwarp();
 }
 
 __global__ void __launch_bounds__(kAtThreads, 1)
@@ -235,7 +282,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   __shared__ uint32_t tmem_slot, gave_up, last_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t q_tile = base, k_ring = base + 2 * kTileBytes, v_ring = k_ring + kAtStages * kTileBytes;
+  const uint32_t q_tile = base, k_ring = base + 2 * kTileBytes, v_ring = k_ring + kAtStages * kTileBytes,
+                 rows_out = v_ring + kAtStages * kTileBytes;
 
   if (tid == 0) {
     mbar_init(&q_full, 1);
@@ -258,7 +306,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   }
   if (warp == 12) tmem_alloc512(&tmem_slot);
   tmem_fence_before();
-  at_make_plan(pl, p, tid);  // ends with a barrier of the block
+  at_make_plan(pl, p, reinterpret_cast<long long*>(smem_raw + (base - smem_addr(smem_raw))), tid);  // ends with a barrier
   tmem_fence_after();
   const uint32_t tmem = tmem_slot;  // columns: S0 | S1 | O0 | O1, 128 each
 
@@ -382,45 +430,45 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
         }
         if (warp_live && !(merge && t == 1)) {
-          const int64_t row = (int64_t)(pl.first[sg.u.b] + sg.u.tok0 + tok) * p.c.Hq + sg.u.h * G + rg;
+          const int64_t row = (int64_t)(sg.u.row0 + tok) * p.c.Hq + sg.u.h * G + rg;
           float* st = p.part + ((int64_t)sg.slot * p.part_rows + (tok * G + rg)) * kAtPartRow;
           if (!sg.part) {
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;  // a row that sees nothing: O is 0 as well
             fa *= inv;
             fb *= inv;
           }
+          const uint32_t buf = rows_out + warp * kAtRowsOut;
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t x[32];
-            tmem_ld32(O + c, x);
-            tmem_wait_ld(x);
-            if (merge) {
-              uint32_t y[32];
-              tmem_ld32(O + 128 + c, y);
-              tmem_wait_ld(y);
+          for (int c0 = 0; c0 < 128; c0 += 64) {
+            uint32_t y[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                x[i] = __float_as_uint(__uint_as_float(x[i]) * fa + __uint_as_float(y[i]) * fb);
-            } else {
+            for (int hf = 0; hf < 2; ++hf) {
+              const int c = c0 + 32 * hf;
+              uint32_t x[32];
+              tmem_ld32(O + c, x);
+              tmem_wait_ld(x);
+              if (merge) {
+                uint32_t z[32];
+                tmem_ld32(O + 128 + c, z);
+                tmem_wait_ld(z);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fa);
+                for (int i = 0; i < 32; ++i)
+                  x[i] = __float_as_uint(__uint_as_float(x[i]) * fa + __uint_as_float(z[i]) * fb);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fa);
+              }
+              if (sg.part) {
+                at_store_rows(buf, x, live ? st + 4 + c : nullptr, lane);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                      : "=r"(y[16 * hf + i])
+                      : "f"(__uint_as_float(x[2 * i + 1])), "f"(__uint_as_float(x[2 * i])));
+              }
             }
-            if (!live) continue;
-            if (!sg.part) {
-              uint32_t y[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-                    : "=r"(y[i])
-                    : "f"(__uint_as_float(x[2 * i + 1])), "f"(__uint_as_float(x[2 * i])));
-              uint4* o = reinterpret_cast<uint4*>(p.c.out + row * kDim + c);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                reinterpret_cast<uint4*>(st + 4 + c)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-            }
+            if (!sg.part) at_store_rows(buf, y, live ? p.c.out + row * kDim + c0 : nullptr, lane);
           }
           if (live) {
             if (sg.part) *reinterpret_cast<float2*>(st) = make_float2(m, l);
@@ -455,7 +503,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             float o[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = 0.0f;
-#pragma unroll 2
+#pragma unroll 5
             for (int c = sg.ca; c <= sg.cb; ++c) {
               const float2 ml = __ldcg(reinterpret_cast<const float2*>(st));
               float4 x[4];
@@ -477,7 +525,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
             const float inv = L > 0.0f ? 1.0f / L : 0.0f;
             const int tk = pr / G;
-            const int64_t row = (int64_t)(pl.first[sg.u.b] + sg.u.tok0 + tk) * p.c.Hq + sg.u.h * G + (pr - tk * G);
+            const int64_t row = (int64_t)(sg.u.row0 + tk) * p.c.Hq + sg.u.h * G + (pr - tk * G);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t y0, y1;
@@ -508,7 +556,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       while (at_next(pl, p, w, sg)) {
         if (!is_v && lt == 0) {  // Q: TQ tokens' heads of the group are TQ * G rows of a tile
           mbar_wait_or_give_up(&q_empty, (nseg & 1) ^ 1, &gave_up);
-          const int nt = sg.u.ntok > p.TQ ? 2 : 1, tok = pl.first[sg.u.b] + sg.u.tok0;
+          const int nt = sg.u.ntok > p.TQ ? 2 : 1, tok = sg.u.row0;
           mbar_arrive_expect_tx(&q_full, (uint32_t)(nt * p.TQ * p.c.G * 2 * kDim));
           for (int t = 0; t < nt; ++t) {
             tma_load_3d(q_tile + t * kTileBytes, &q_map, 0, sg.u.h * p.c.G, tok + t * p.TQ, &q_full);
