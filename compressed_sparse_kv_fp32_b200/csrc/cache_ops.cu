@@ -16,6 +16,8 @@ int cuda_fail(cudaError_t e);  // adamas.cu: records the error, returns ADAMAS_E
 
 static_assert(kErrOffsets == ADAMAS_DEVERR_OFFSETS, "error bits of the header");
 
+constexpr int kCopyBlocks = 148 * 8;
+constexpr int64_t kRopeSplitBlocks = 592;  // blocks up to which a token's rows are split: four per multiprocessor
 constexpr size_t kCtrlBytes = 256;  // control words at the start of every workspace
 
 static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -52,6 +54,41 @@ static int check_ctrl(const void* ws, size_t bytes, size_t need) {
 }
 
 static uint32_t* err_word(void* ws) { return static_cast<uint32_t*>(ws) + 2; }
+
+// A launch in clusters of C blocks; `most` bytes of dynamic shared memory are allowed to
+// the kernel once per device.
+template <auto Kernel, typename... Args>
+static int launch_cluster(int grid, int C, int threads, size_t smem, size_t most, cudaStream_t st, Args... args) {
+  cudaError_t e;
+  if (most > 48 * 1024) {
+    static std::atomic<uint64_t> known{0};  // a bit per device
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(known.load(std::memory_order_acquire) & bit) || bit == 0) {
+      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(Kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+      if (e != cudaSuccess) return cuda_fail(e);
+      known.fetch_or(bit, std::memory_order_release);
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, Kernel, args...)) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return cuda_fail(e);
+  }
+  return ADAMAS_OK;
+}
 
 static int launched() {
   const cudaError_t e = cudaGetLastError();
@@ -204,7 +241,6 @@ int adamas_rope_append(const adamas_rope_args* args, adamas_stream_t stream) {
   p.positions = a.positions;
   p.freqs = a.freqs;
   p.rot = a.rot_dim;
-  p.interleaved = a.interleaved != 0;
   p.mscale = a.mscale;
   p.T = a.T;
   p.B = a.B;
@@ -215,7 +251,18 @@ int adamas_rope_append(const adamas_rope_args* args, adamas_stream_t stream) {
   p.V = static_cast<uint16_t*>(a.V);
   p.codes = a.codes;
   p.err = err_word(a.workspace);
-  rope_append_kernel<<<dim3((unsigned)a.T, 1), kRopeThreads, 0, (cudaStream_t)stream>>>(p);
+  // many tokens: kRopeTokens to a block; a few: one, and its rows over more blocks, down to
+  // two rows a warp, as the rows of a warp come one after the other
+  const int pairs = ((p.q ? a.Hq : 0) + (p.k ? 2 * a.Hkv : 0) + 1) / 2, warps = kRopeThreads / 32;
+  int split = (pairs + warps - 1) / warps;
+  if ((int64_t)split * a.T > kRopeSplitBlocks) split = (int)(kRopeSplitBlocks / a.T > 0 ? kRopeSplitBlocks / a.T : 1);
+  p.neg0 = 0x8000000080000000ull;
+  p.tokens = a.T >= kRopeSplitBlocks * kRopeTokens ? kRopeTokens : 1;
+  const dim3 grid((unsigned)((a.T + p.tokens - 1) / p.tokens), (unsigned)split);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (a.interleaved) rope_append_kernel<kRopeInside><<<grid, kRopeThreads, 0, st>>>(p);
+  else if (a.rot_dim % 16 == 0) rope_append_kernel<kRopeShuffle><<<grid, kRopeThreads, 0, st>>>(p);
+  else rope_append_kernel<kRopeLoad><<<grid, kRopeThreads, 0, st>>>(p);
   return launched();
 }
 
@@ -299,8 +346,19 @@ int adamas_accumulate_kept(const adamas_kept_args* args, adamas_stream_t stream)
   p.shared_rows = a.policy == ADAMAS_SELECT_GROUP_SHARED;
   p.mass = a.mass;
   p.err = err_word(a.workspace);
-  accumulate_kept_kernel<<<(unsigned)(a.B * a.Hkv), 256, 0, (cudaStream_t)stream>>>(p);
-  return launched();
+  // blocks of a kv head: up to about two per multiprocessor in all, 64 slots of a list each
+  // at least; more when a block's scores would not fit
+  const int heads = a.B * a.Hkv;
+  int C = 1;
+  while (C < kKeptCluster && (int64_t)heads * 2 * C <= 296 && a.budget >= 128 * C) C *= 2;
+  while (C < kKeptCluster && (int64_t)((a.budget + C - 1) / C) * p.G > kKeptSmemFloats) C *= 2;
+  const int cap = (a.budget + C - 1) / C;
+  if ((int64_t)cap * p.G > kKeptSmemFloats) {
+    accumulate_kept_large_kernel<<<(unsigned)heads, 256, 0, (cudaStream_t)stream>>>(p);
+    return launched();
+  }
+  return launch_cluster<accumulate_kept_kernel>(heads * C, C, kKeptThreads, (size_t)cap * p.G * sizeof(float),
+                        kKeptSmemFloats * sizeof(float), (cudaStream_t)stream, p, cap);
 }
 
 int adamas_evict(const adamas_evict_args* args, adamas_stream_t stream) {
@@ -350,9 +408,26 @@ int adamas_evict(const adamas_evict_args* args, adamas_stream_t stream) {
   p.codes_out = in_place ? a.codes : a.codes_out;
   p.mass_out = in_place ? a.mass : a.mass_out;
   p.err = err_word(a.workspace);
-  const unsigned grid = (unsigned)(a.B * a.Hkv);
-  evict_select_kernel<<<grid, kSelThreads, 0, (cudaStream_t)stream>>>(p);
-  evict_move_kernel<<<grid, kMoveThreads, 0, (cudaStream_t)stream>>>(p);
+  cudaStream_t st = (cudaStream_t)stream;
+  const int heads = a.B * a.Hkv;
+  int C = (int)((p.geo.Nmax + kSelBlockTokens - 1) / kSelBlockTokens);
+  C = C < 1 ? 1 : (C > kSelCluster ? kSelCluster : C);
+  const int64_t slice = (p.geo.Nmax + C - 1) / C;
+  const size_t keys = slice <= kSelSmemTokens ? (size_t)slice * sizeof(uint32_t) : 0;
+  if ((rc = launch_cluster<evict_select_kernel>(heads * C, C, kSelThreads, keys, kSelSmemTokens * sizeof(uint32_t), st,
+                           p)) != ADAMAS_OK)
+    return rc;
+  if (in_place) {  // a cluster per head, up to about one block per multiprocessor in all
+    C = 1;
+    while (C < 8 && (int64_t)heads * 2 * C <= 148 && a.keep >= 64 * C) C *= 2;
+    return launch_cluster<evict_shift_kernel>(heads * C, C, kShiftThreads, 0, 0, st, p);
+  }
+  // 64 rows a block and round, about eight rounds when there are many
+  int per_head = (a.keep + 63) / 64;
+  const int most = kCopyBlocks / heads;
+  if (per_head > most) per_head = most;
+  if (per_head < 1) per_head = 1;
+  evict_copy_kernel<<<(unsigned)(heads * per_head), kMoveThreads, 0, st>>>(p, per_head);
   return launched();
 }
 

@@ -22,14 +22,16 @@ struct RopeParams {
   int64_t q_stride, k_stride, v_stride;
   const int32_t *cu_new, *cache_lens, *positions;
   const uint64_t* freqs;
-  int rot, interleaved;
+  int rot;
   double mscale;
   int T, B, Hq, Hkv;
+  int tokens;  // of a block
   uint16_t* q_out;
   uint16_t *K, *V;
   uint8_t* codes;
   CacheGeom geo;
   uint32_t* err;
+  uint64_t neg0;  // -0 twice
 };
 
 constexpr int kRopeThreads = 256;
@@ -40,112 +42,210 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return r;
 }
 
-// The lane's four elements 4 lane .. 4 lane + 3 of a row, rotated.  cs holds (c, s)
-// of every pair; x is the row (read again for partners that no single lane holds).
-__device__ __forceinline__ uint2 rope_row(const uint16_t* x, uint2 raw, const float2* cs, int rot, int interleaved,
-                                          int lane) {
-  float v[4] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y)};
-  float o[4];
-  const int half = rot >> 1, e0 = 4 * lane;
-  if (interleaved) {
+// Sixteen lanes hold a row, eight elements 8 l .. 8 l + 7 each, so that a warp has two
+// rows in hand.  How a lane gets its elements' partners:
+constexpr int kRopeShuffle = 0;  // half layout, rot % 16 == 0: they are one other lane's elements
+constexpr int kRopeInside = 1;   // interleaved: its own
+constexpr int kRopeLoad = 2;     // half layout, other rot: read from the row again
+
+__device__ __forceinline__ uint64_t bf16_to_f2(uint32_t w) { return f2_pack(bf16_lo(w), bf16_hi(w)); }
+
+// What a lane needs of its token, the same for every row: cos and signed sin of its
+// elements in pairs (x' = x c + partner s with s negative for the first of a rotated pair:
+// the product's sign is exact, so this is the difference of the definition bit for bit).
+struct RopeLane {
+  uint64_t c[4], s[4];
+  // A packed multiplication followed by a packed addition came out as one fused operation,
+  // whose result can be a rounding off.  Here a product is a fused operation with a -0
+  // that the compiler does not know: the rounded product, and not to be merged.
+  uint64_t neg0;
+  uint32_t on;  // bit i: elements 2 i and 2 i + 1 are rotated
+};
+
+template <int MODE>
+__device__ __forceinline__ uint4 rope_row(const uint16_t* x, uint4 raw, const RopeLane& t, int partner, int rot, int l) {
+  const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      o[i] = v[i];
-      o[i + 1] = v[i + 1];
-      if (e0 + i < rot) {
-        const float2 t = cs[(e0 + i) >> 1];
-        o[i] = __fsub_rn(__fmul_rn(v[i], t.x), __fmul_rn(v[i + 1], t.y));
-        o[i + 1] = __fadd_rn(__fmul_rn(v[i + 1], t.x), __fmul_rn(v[i], t.y));
-      }
-    }
-  } else {
-    float w[4];  // the partners
-    if ((half & 3) == 0) {  // the partner of a lane's elements is one lane's elements
-      const int d = half >> 2;
-      const int src = e0 < half ? lane + d : lane - d;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __shfl_sync(0xffffffffu, v[i], src & 31);
+  for (int i = 0; i < 4; ++i) {
+    uint64_t w;
+    if constexpr (MODE == kRopeShuffle) {
+      w = bf16_to_f2(__shfl_sync(0xffffffffu, v[i], partner));
+    } else if constexpr (MODE == kRopeInside) {
+      w = f2_pack(bf16_hi(v[i]), bf16_lo(v[i]));
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = e0 + i, p = e < half ? e + half : e - half;
-        w[i] = e < rot ? __uint_as_float((uint32_t)x[p] << 16) : 0.0f;
+      const int e = 8 * l + 2 * i, half = rot >> 1;
+      float a = 0.0f, b = 0.0f;
+      if (e < rot) {  // rot is even: the pair is rotated or not
+        a = __uint_as_float((uint32_t)x[e < half ? e + half : e - half] << 16);
+        b = __uint_as_float((uint32_t)x[e + 1 < half ? e + 1 + half : e + 1 - half] << 16);
       }
+      w = f2_pack(a, b);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = e0 + i;
-      o[i] = v[i];
-      if (e < half) {
-        const float2 t = cs[e];
-        o[i] = __fsub_rn(__fmul_rn(v[i], t.x), __fmul_rn(w[i], t.y));
-      } else if (e < rot) {
-        const float2 t = cs[e - half];
-        o[i] = __fadd_rn(__fmul_rn(v[i], t.x), __fmul_rn(w[i], t.y));
-      }
-    }
+    float a, b;
+    f2_unpack(f2_add(f2_fma(bf16_to_f2(v[i]), t.c[i], t.neg0), f2_fma(w, t.s[i], t.neg0)), a, b);
+    // unrotated elements keep their bits (a NaN's payload too)
+    o[i] = t.on >> i & 1 ? bf16_pair(a, b) : v[i];
   }
-  // unrotated elements keep their bits (a NaN's payload too)
-  uint2 r = make_uint2(bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3]));
-  if (e0 >= rot) r.x = raw.x;
-  if (e0 + 2 >= rot) r.y = raw.y;
-  return r;
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// One block per token (grid.x) and share of its rows (grid.y): the block's threads
-// evaluate the token's cos and sin, then each warp takes rows of the Hq query heads,
-// the Hkv keys and the Hkv values in turn.
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p) {
-  __shared__ float2 cs[kDim / 2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = blockIdx.x;
-  // the sequence of row r: the last one that starts at or before it
-  int below = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kRopeThreads)
-    below += __syncthreads_count(b0 + tid < p.B && p.cu_new[b0 + tid] <= r);
-  const int b = below - 1;
-  if (b < 0) return;  // a row before the first sequence
-  int first, n;
-  bool bad = false;
-  ragged_rows(p.cu_new, b, p.T, first, n, bad);
-  if (bad && p.err && tid == 0) atomicOr(p.err, kErrOffsets);
-  if (r < first || r >= first + n) return;  // behind the last sequence
-  const int64_t slot64 = (int64_t)p.cache_lens[b] + (r - first);
-  const int pos = p.positions ? p.positions[r] : (int)slot64;
-  if (tid < p.rot / 2) {
-    const uint64_t turn = p.freqs[tid] * (uint64_t)(int64_t)pos;
-    double s, c;
-    sincospi((double)(int64_t)turn * 0x1p-63, &s, &c);
-    cs[tid] = make_float2((float)(c * p.mscale), (float)(s * p.mscale));
+// The 2-bit codes of the row in each half of a warp: the arithmetic of encode128_warp
+// (stage h pairs elements h apart, ascending; then one multiplication), stages 1, 2, 4
+// inside a lane, 8 .. 64 between lanes.  Returns the lane's eight codes in 16 bits, in
+// the order of the packed bytes.
+__device__ __forceinline__ uint32_t encode128_half(uint4 raw, int l) {
+  float v[8] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y),
+                bf16_lo(raw.z), bf16_hi(raw.z), bf16_lo(raw.w), bf16_hi(raw.w)};
+#pragma unroll
+  for (int h = 1; h < 8; h *= 2)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & h)) {
+        const float a = v[i], b = v[i + h];
+        v[i] = __fadd_rn(a, b);
+        v[i + h] = __fsub_rn(a, b);
+      }
+#pragma unroll
+  for (int m = 1; m < 16; m *= 2) {  // h = 8 m: the upper lane holds x[j + h] and gets x[j] - x[j + h]
+    const bool upper = (l & m) != 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = __shfl_xor_sync(0xffffffffu, v[i], m);
+      v[i] = __fadd_rn(q, upper ? -v[i] : v[i]);  // the same as q - v and, addition commuting, v + q
+    }
+  }
+  const float c = hadamard_norm();
+  float mx = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = __fmul_rn(v[i], c);
+    mx = fmaxf(mx, fabsf(v[i]));
+  }
+#pragma unroll
+  for (int m = 8; m > 0; m /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+  const float t0 = -0.5f * mx, t2 = 0.5f * mx;
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w |= code_of(v[i], t0, t2) << ((i < 4 ? 6 : 14) - 2 * (i & 3));
+  return w;
+}
+
+// A block has kRopeTokens tokens, two warps each, or, when there are few tokens, one, whose
+// rows may be shared by several blocks (grid.y).  While a warp's first rows (of the Hq
+// query heads, the Hkv keys and the Hkv values in turn, two at a time) are on their way,
+// two warps per token find its sequence and place and evaluate its cos and sin; a row's
+// registers are asked for again as soon as it is done.  Bound by instructions and HBM
+// when there are many tokens, by latency for a few.
+constexpr int kRopeAhead = 4;  // pairs of rows
+constexpr int kRopeTokens = kRopeThreads / 64;
+
+template <int MODE>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const RopeParams p) {
+  __shared__ float2 cs[kRopeTokens][kDim / 2];
+  __shared__ int64_t row0_of[kRopeTokens];  // its row in the cache's first head; -1: in no sequence, -2: not stored
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 15, hi = lane >> 4, e0 = 8 * l;
+  const int nq = p.q ? p.Hq : 0, nk = p.k ? p.Hkv : 0, rows = nq + 2 * nk, pairs = (rows + 1) >> 1;
+  const int share = (kRopeThreads / 32) / p.tokens;  // warps of a token: 8 or 2
+  const int tk = warp / share, part = warp - tk * share;
+  const int64_t r = (int64_t)blockIdx.x * p.tokens + tk;
+  const int stride = gridDim.y * share, i0 = r < p.T ? blockIdx.y * share + part : pairs;
+
+  auto source = [&](int i) {
+    return (i < nq ? p.q + r * p.q_stride + i * kDim
+                   : (i < nq + nk ? p.k + r * p.k_stride + (i - nq) * kDim
+                                  : p.v + r * p.v_stride + (i - nq - nk) * kDim)) + e0;
+  };
+  auto ask = [&](int pair) {
+    const int i = 2 * pair + hi;
+    return i < rows ? *reinterpret_cast<const uint4*>(source(i)) : make_uint4(0, 0, 0, 0);
+  };
+  uint4 raw[kRopeAhead];
+#pragma unroll
+  for (int j = 0; j < kRopeAhead; ++j) raw[j] = ask(i0 + j * stride);
+
+  if (part < 2 && r < p.T) {
+    int below = 0;  // the sequence of row r is the last one that starts at or before it
+    for (int b0 = 0; b0 < p.B; b0 += 32)
+      below += __popc(__ballot_sync(0xffffffffu, b0 + lane < p.B && p.cu_new[b0 + lane] <= r));
+    int64_t row0 = -1;
+    if (below > 0) {
+      int first, n;
+      bool bad = false;
+      ragged_rows(p.cu_new, below - 1, p.T, first, n, bad);
+      if (bad && lane == 0) atomicOr(p.err, kErrOffsets);
+      if (r >= first && r < first + n) {
+        const int64_t slot = (int64_t)p.cache_lens[below - 1] + (r - first);
+        const int pair = part * 32 + lane;
+        if (pair < p.rot / 2) {
+          const int pos = p.positions ? p.positions[r] : (int)slot;
+          const uint64_t turn = p.freqs[pair] * (uint64_t)(int64_t)pos;
+          double s, c;
+          sincospi((double)(int64_t)turn * 0x1p-63, &s, &c);
+          cs[tk][pair] = make_float2((float)(c * p.mscale), (float)(s * p.mscale));
+        }
+        row0 = -2;
+        if (nk && slot >= 0 && slot < p.geo.Nmax) {
+          bool bad_page = false;
+          const int64_t row = p.geo.row(below - 1, 0, (int)slot, bad_page);
+          if (!bad_page) row0 = row;
+          else if (lane == 0) atomicOr(p.err, kErrTable);
+        }
+      }
+    }
+    if (part == 0 && lane == 0) row0_of[tk] = row0;
   }
   __syncthreads();
-  const int nq = p.q ? p.Hq : 0, nk = p.k ? p.Hkv : 0;
-  const bool in_cache = slot64 >= 0 && slot64 < p.geo.Nmax;
-  const int rows = nq + 2 * nk;
-  for (int i = blockIdx.y * (kRopeThreads / 32) + warp; i < rows; i += gridDim.y * (kRopeThreads / 32)) {
-    const bool is_q = i < nq, is_k = !is_q && i < nq + nk;
-    const int h = is_q ? i : (is_k ? i - nq : i - nq - nk);
-    const uint16_t* x = is_q ? p.q + r * p.q_stride : (is_k ? p.k + r * p.k_stride : p.v + r * p.v_stride);
-    x += h * kDim;
-    if (!is_q && !in_cache) continue;
-    const uint2 raw = *reinterpret_cast<const uint2*>(x + 4 * lane);
-    uint2 o = raw;
-    if (is_q || is_k) o = rope_row(x, raw, cs, p.rot, p.interleaved, lane);
-    __syncwarp();  // every lane has read the row: q_out may be q
-    if (is_q) {
-      *reinterpret_cast<uint2*>(p.q_out + ((int64_t)r * p.Hq + h) * kDim + 4 * lane) = o;
-      continue;
+  if (i0 >= pairs) return;
+  const int64_t row0 = row0_of[tk];
+  if (row0 == -1) return;
+  const int64_t head_rows = p.geo.table ? p.geo.page.d : p.geo.Nmax;  // from one head's row to the next one's
+  const int half = p.rot >> 1;
+  const int partner = (e0 < half ? lane + (half >> 3) : lane - (half >> 3)) & 31;
+  RopeLane t;
+  t.on = 0;
+  t.neg0 = p.neg0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float c[2], s[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int e = e0 + 2 * k + m;
+      const bool second = MODE == kRopeInside ? m : e >= half;
+      const float2 z = e < p.rot ? cs[tk][MODE == kRopeInside ? e >> 1 : (second ? e - half : e)] : make_float2(1.0f, 0.0f);
+      c[m] = z.x;
+      s[m] = second ? z.y : -z.y;
     }
-    bool bad_page = false;
-    const int64_t row = p.geo.row(b, h, (int)slot64, bad_page);
-    if (bad_page) {
-      if (p.err && lane == 0) atomicOr(p.err, kErrTable);
-      continue;
-    }
-    *reinterpret_cast<uint2*>((is_k ? p.K : p.V) + row * kDim + 4 * lane) = o;
-    if (is_k && p.codes) {
-      const uint32_t w = encode128_warp_raw(o, lane);
-      if (lane < kCodeWords) reinterpret_cast<uint32_t*>(p.codes + row * kCodeBytes)[lane] = w;
+    t.c[k] = f2_pack(c[0], c[1]);
+    t.s[k] = f2_pack(s[0], s[1]);
+    t.on |= (uint32_t)(e0 + 2 * k < p.rot) << k;
+  }
+  for (int p0 = i0; p0 < pairs; p0 += kRopeAhead * stride) {
+#pragma unroll
+    for (int j = 0; j < kRopeAhead; ++j) {
+      const int pair = p0 + j * stride, i = 2 * pair + hi;
+      if (pair >= pairs) break;
+      const uint4 in = raw[j];
+      const bool rotate = i < nq + nk, some = 2 * pair < nq + nk;
+      uint4 o = in;
+      if (some) {
+        o = rope_row<MODE>(MODE == kRopeLoad ? source(rotate ? i : 2 * pair) - e0 : nullptr, in, t, partner, p.rot, l);
+        if (!rotate) o = in;
+        if (MODE == kRopeLoad) __syncwarp();  // every lane has read the row: q_out may be q
+      }
+      if (p0 + kRopeAhead * stride < pairs) raw[j] = ask(pair + kRopeAhead * stride);
+      if (i < nq) {
+        *reinterpret_cast<uint4*>(p.q_out + (r * p.Hq + i) * kDim + e0) = o;
+      } else if (row0 >= 0 && i < rows) {
+        const int64_t row = row0 + (rotate ? i - nq : i - nq - nk) * head_rows;
+        *reinterpret_cast<uint4*>((rotate ? p.K : p.V) + row * kDim + e0) = o;
+      }
+      if (p.codes && some && 2 * pair + 1 >= nq && row0 >= 0) {  // a key among the two rows
+        uint32_t w = encode128_half(o, l);
+        w |= __shfl_down_sync(0xffffffffu, w, 1) << 16;
+        if (i >= nq && rotate && (l & 1) == 0)
+          reinterpret_cast<uint32_t*>(p.codes + (row0 + (i - nq) * head_rows) * kCodeBytes)[l >> 1] = w;
+      }
     }
   }
 }

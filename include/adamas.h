@@ -370,8 +370,8 @@ int adamas_merge_partials(const float *partials, int n, int B, int Hq, float *ou
  *   - A ragged batch of new tokens is packed: sequence b owns rows
  *     [cu[b], cu[b + 1]) of the T rows, cu device int32 [B + 1], ascending within
  *     [0, T] (else ADAMAS_DEVERR_OFFSETS, and the sequence is left out).  Rows
- *     before cu[0] and from cu[B] on belong to no sequence: nothing is read from
- *     them and their outputs are left as they were.
+ *     before cu[0] and from cu[B] on belong to no sequence: their values play no
+ *     part and their outputs are left as they were.
  *   - mass device fp32 [B][Hkv][Nmax] (paged: Nmax = max_pages * page_size, by slot
  *     and not by page): the attention weight a token received so far, summed over
  *     query rows and over the query heads of its kv head.

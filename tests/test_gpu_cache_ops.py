@@ -314,6 +314,8 @@ def test_bindings_refuse():
     (1, 8, 1, 5000, [5000], 1024, 64, False),
     (1, 4, 4, 9000, [9000], 9000, 0, False),
     (2, 5, 1, 700, [700, 500], 333, 1, False),
+    (1, 8, 1, 60000, [60000], 60000, 0, False),           # longer lists than a cluster's shared memory holds
+    (1, 8, 1, 60000, [60000], 60000, 0, True),
 ])
 def test_accumulate_kept(B, Hq, Hkv, N, lens, budget, page, shared):
     rng = np.random.default_rng(31)
@@ -356,6 +358,8 @@ EVICT = [
     (2, [5000, 4999], 5000, 4500, 16, 0, 24, None, False),
     (1, [40000], 40000, 20000, 4, 128, 0, None, True),
     (4, [9000, 130, 9000], 9000, 4096, 4, 64, 1, 16, True),
+    (1, [400000], 400000, 700, 4, 64, 0, 0, True),             # a block's slice does not fit its shared memory
+    (1, [330000], 330000, 329000, 0, 0, 16, None, False),
     (16, [3000, 2999, 1, 3000, 64, 500, 2000, 3000, 2048, 7], 3000, 1024, 0, 0, 0, None, True),
 ]
 
