@@ -219,24 +219,28 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 // ---------------------------------------------------------------- which tokens stay
 // A cluster of blocks per (b, kv head), a slice of the tokens each.  The keys are read
 // once into shared memory (a slice that does not fit is read again).  The k-th largest key
-// is found by four 8-bit digits, most significant first: the blocks count their keys
-// under the digits known so far, each takes the cluster's counts from its peers, and one
-// warp finds the digit.  Then every warp counts what it keeps of its run of tokens, and
-// writes the kept slots in ascending order behind those of the warps and blocks before it.
-// Bound by latency: about five exchanges between blocks.
+// is found by 8-bit digits, most significant first: the blocks count their keys under the
+// digits known so far, each adds up the cluster's counts, and one warp finds the digit;
+// the rest of the digits need not be known once all keys under them are kept.  Then every
+// warp counts what it keeps of its run of tokens, and writes the kept slots in ascending
+// order behind those of the warps and blocks before it.  Bound by latency: up to five
+// exchanges between blocks.  (Digits of 11 bits, one exchange less, took twice as long:
+// the counts of eight blocks are then 64 KB a block and exchange.)
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBlockTokens = 2048;  // a block more for so many tokens, up to 8
 constexpr int kSelCluster = 8;
 constexpr int kSelSmemTokens = 40960;  // keys of a slice kept in shared memory
+constexpr int kSelBins = 256;
 constexpr int kSelCopies = 8;          // counters of a digit, by lane, as lanes often agree
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t sm_key[];
-  __shared__ uint32_t hist[256 * kSelCopies];
-  __shared__ uint32_t total[256];
-  __shared__ uint32_t s_digit, s_above;
+  __shared__ uint32_t hist[kSelBins * kSelCopies];
+  __shared__ uint32_t total[2][kSelBins];  // of even and odd digits: a peer may still read the last one's
+  __shared__ uint32_t sums[kSelBins];      // the cluster's counts
+  __shared__ uint32_t s_digit, s_above, s_all;
   __shared__ int s_count[2];          // this block's tokens above the k-th key, and equal to it
   __shared__ int wsum[2][kSelWarps];
   cg::cluster_group cluster = cg::this_cluster();
@@ -274,27 +278,38 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   int need = k;  // of the tokens whose digits so far equal prefix, this many are kept
 #pragma unroll 1
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256 * kSelCopies; i += kSelThreads) hist[i] = 0;
+    for (int i = tid; i < kSelBins * kSelCopies; i += kSelThreads) hist[i] = 0;
     __syncthreads();
     for (int t = t0 + tid; t < t1; t += kSelThreads) {
       const uint32_t u = key(t);
       if ((u & mask) == prefix) atomicAdd(&hist[((u >> shift) & 255) * kSelCopies + (lane & (kSelCopies - 1))], 1u);
     }
     __syncthreads();
-    if (tid < 256) {
+    uint32_t* mine = total[(shift >> 3) & 1];
+    if (tid < kSelBins) {
       uint32_t s = 0;
 #pragma unroll
       for (int c = 0; c < kSelCopies; ++c) s += hist[tid * kSelCopies + c];
-      total[tid] = s;
+      mine[tid] = s;
+      if (C == 1) sums[tid] = s;
     }
-    cluster.sync();
+    if (C > 1) {
+      cluster.sync();
+      if (tid < kSelBins) {
+        uint32_t s = 0;
+#pragma unroll
+        for (int c = 0; c < kSelCluster; ++c)
+          if (c < C) s += cluster.map_shared_rank(mine, c)[tid];
+        sums[tid] = s;
+      }
+    }
+    __syncthreads();
     if (warp == 0) {
-      // lane l: digits 255 - 8 l down to 248 - 8 l, summed over the blocks
+      // lane l: digits 255 - 8 l down to 248 - 8 l
       uint32_t d[8], sum = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        d[i] = 0;
-        for (int c = 0; c < C; ++c) d[i] += cluster.map_shared_rank(total, c)[255 - 8 * lane - i];
+        d[i] = sums[255 - 8 * lane - i];
         sum += d[i];
       }
       uint32_t inc = sum;
@@ -303,27 +318,37 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
         const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
-      const uint32_t here = __ballot_sync(0xffffffffu, inc >= (uint32_t)need);
-      if (lane == __ffs(here) - 1) {
-        uint32_t above = inc - sum;
-        int i = 0;
-        while (i < 7 && above + d[i] < (uint32_t)need) above += d[i++];
-        s_digit = 255 - 8 * lane - i;
-        s_above = above;
+      if (lane == __ffs(__ballot_sync(0xffffffffu, inc >= (uint32_t)need)) - 1) {
+        uint32_t above = inc - sum, found = 0, at = 7, before = 0;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {  // the first i whose running count reaches need
+          uint32_t run = above;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) run += j < i ? d[j] : 0;
+          if (run + d[i] >= (uint32_t)need) {
+            at = i;
+            before = run;
+            found = d[i];
+          }
+        }
+        s_digit = 255 - 8 * lane - at;
+        s_above = before;
+        s_all = before + found == (uint32_t)need;
       }
     }
-    cluster.sync();  // the peers' counts are read before they change
+    __syncthreads();
     prefix |= s_digit << shift;
     mask |= 255u << shift;
     need -= (int)s_above;
+    if (s_all) break;  // every key under these digits is kept
   }
 
-  // kept: key > prefix, and the first `need` of key == prefix; each warp has a run of tokens
+  // kept: (key & mask) > prefix, and the first `need` that equal it; each warp has a run of tokens
   const int run = ((t1 - t0 + kSelThreads - 1) / kSelThreads) * 32;
   const int w0 = t0 + warp * run, w1 = w0 + run < t1 ? w0 + run : t1;
   int gt = 0, eq = 0;
   for (int t = w0 + lane; t < w1; t += 32) {
-    const uint32_t u = key(t);
+    const uint32_t u = key(t) & mask;
     gt += u > prefix;
     eq += u == prefix;
   }
@@ -352,7 +377,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   }
   const uint32_t lt = (1u << lane) - 1u;
   for (int t = w0 + lane; t - lane < w1; t += 32) {
-    const uint32_t u = t < w1 ? key(t) : 0u;
+    const uint32_t u = t < w1 ? key(t) & mask : 0u;
     const bool g = t < w1 && u > prefix, e = t < w1 && u == prefix;
     const uint32_t bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
     const int te = ties + __popc(be & lt);  // ties before this token: the first `need` of them are kept
@@ -400,11 +425,13 @@ __device__ __forceinline__ void move_group(MoveGroup& m, const EvictParams& p, i
   }
 }
 
-// To another cache: any block may move any rows.  Bound by HBM (2 x 548 bytes a token).
+// To another cache: any block may move any rows.  A warp has kMoveGroups groups of rows on
+// their way at a time, and looks up where the next ones are meanwhile.  Bound by HBM
+// (2 x 548 bytes a token).
 constexpr int kMoveThreads = 256;
-constexpr int kMoveGroups = 2;  // groups a warp has under way
+constexpr int kMoveGroups = 2;
 
-__global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictParams p, int blocks_per_head) {
+__global__ void __launch_bounds__(kMoveThreads, 3) evict_copy_kernel(const EvictParams p, int blocks_per_head) {
   constexpr int kWarps = kMoveThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hk = blockIdx.x / blocks_per_head, part = blockIdx.x - hk * blocks_per_head;
@@ -414,31 +441,40 @@ __global__ void __launch_bounds__(kMoveThreads) evict_copy_kernel(const EvictPar
   const int k = p.keep < len ? p.keep : len;
   bad = false;
   const int32_t* kept = p.kept + (int64_t)hk * p.keep;
-  const int step = blocks_per_head * kWarps * 4;
-  for (int j0 = (part * kWarps + warp) * 4; j0 < k; j0 += kMoveGroups * step) {
-    MoveGroup m[kMoveGroups];
-    int64_t to[kMoveGroups];
+  const int step = blocks_per_head * kWarps * 4;  // rows of a round of all warps
+  int64_t from[kMoveGroups], to[kMoveGroups];
+  int slot[kMoveGroups];
+  auto look_up = [&](int j0) {
 #pragma unroll
     for (int g = 0; g < kMoveGroups; ++g) {
-      const int j = j0 + g * step, cnt = k - j < 4 ? k - j : 4;
-      int64_t from = -1;
-      int slot = 0;
-      to[g] = -1;
-      if (lane < cnt) {
+      const int j = j0 + g * step + lane;
+      from[g] = to[g] = -1;
+      slot[g] = 0;
+      if (lane < 4 && j < k) {
         bool bad_to = false;
-        slot = kept[j + lane];
-        from = p.geo.row(b, h, slot, bad);
-        to[g] = p.out.row(b, h, j + lane, bad_to);
+        slot[g] = kept[j];
+        from[g] = p.geo.row(b, h, slot[g], bad);
+        to[g] = p.out.row(b, h, j, bad_to);
         if (bad_to) to[g] = -1;  // nothing is written through a bad entry
         bad |= bad_to;
       }
-      move_group<true>(m[g], p, from, cnt, slot, hk, lane);
     }
+  };
+  auto count = [&](int j) { return k - j < 4 ? (k - j < 0 ? 0 : k - j) : 4; };
+  int j0 = (part * kWarps + warp) * 4;
+  look_up(j0);
+  for (; j0 < k; j0 += kMoveGroups * step) {
+    MoveGroup m[kMoveGroups];
+    int64_t dst[kMoveGroups];
 #pragma unroll
     for (int g = 0; g < kMoveGroups; ++g) {
-      const int j = j0 + g * step;
-      move_group<false>(m[g], p, to[g], k - j < 4 ? k - j : 4, j + lane, hk, lane);
+      move_group<true>(m[g], p, from[g], count(j0 + g * step), slot[g], hk, lane);
+      dst[g] = to[g];
     }
+    look_up(j0 + kMoveGroups * step);
+#pragma unroll
+    for (int g = 0; g < kMoveGroups; ++g)
+      move_group<false>(m[g], p, dst[g], count(j0 + g * step), j0 + g * step + lane, hk, lane);
   }
   float* mass_out = p.mass_out + (int64_t)hk * p.out.Nmax;
   for (int64_t t = k + part * kMoveThreads + threadIdx.x; t < p.out.Nmax; t += (int64_t)blocks_per_head * kMoveThreads)
