@@ -7,6 +7,7 @@
 
 #include "../../include/adamas.h"
 #include "chunk_attend.cuh"
+#include "chunk_weights.cuh"
 #include "evict.cuh"
 #include "rope.cuh"
 
@@ -95,8 +96,8 @@ static int launched() {
   return e != cudaSuccess ? cuda_fail(e) : ADAMAS_OK;
 }
 
-// Multiprocessors of the current device, with the one-time set-up of chunk attention's
-// kernel on it: its shared memory, and the register count its split is made for.
+// Multiprocessors of the current device, with the one-time set-up of the chunk kernels on
+// it: their shared memory, and the register count that chunk attention's split is made for.
 static int attend_device(int* sms) {
   static std::atomic<int> known[64];
   int dev = 0;
@@ -108,6 +109,8 @@ static int attend_device(int* sms) {
   cudaFuncAttributes fa;
   if ((e = cudaFuncGetAttributes(&fa, fn)) != cudaSuccess ||
       (e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAtSmem)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&chunk_weights_kernel),
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWtSmem)) != cudaSuccess ||
       (e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return cuda_fail(e);
   if (fa.numRegs != 65536 / kAtThreads) return ADAMAS_ERR_UNSUPPORTED;  // the warps' shares add up to 65536
@@ -164,6 +167,10 @@ static int rows_box(const CacheGeom& g, int page_size) {
   if (g.table)
     while (box >= 8 && page_size % box != 0) box >>= 1;
   return box >= 8 ? box : 0;
+}
+
+static int64_t cache_rows(const adamas_chunk_args& a, const CacheGeom& g) {
+  return a.block_table ? a.n_pages * a.Hkv * a.page_size : (int64_t)a.B * a.Hkv * g.Nmax;
 }
 
 // Workspace of chunk attention: control words | arrival counters | partial states.
@@ -290,7 +297,7 @@ int adamas_chunk_attend(const adamas_chunk_args* args, adamas_stream_t stream) {
   ap.part = reinterpret_cast<float*>(ws + kCtrlBytes + kAtArrivedBytes);
   ap.part_rows = part_rows(a.T, p.G);
   ap.TQ = 128 / p.G;
-  const int64_t rows = a.block_table ? a.n_pages * p.Hkv * a.page_size : (int64_t)a.B * p.Hkv * p.geo.Nmax;
+  const int64_t rows = cache_rows(a, p.geo);
   if (rows > INT32_MAX) return ADAMAS_ERR_UNSUPPORTED;
   CUtensorMap q_map = {}, k_map = {}, v_map = {};
   if ((rc = query_map(a.q, a.T, a.Hq, p.G, ap.TQ, &q_map)) != ADAMAS_OK) return rc;
@@ -314,8 +321,20 @@ int adamas_accumulate_chunk(const adamas_chunk_args* args, adamas_stream_t strea
   if (rc != ADAMAS_OK || a.B == 0 || a.T == 0 || p.geo.Nmax == 0) return rc;
   if ((rc = check_ctrl(a.workspace, a.workspace_bytes, kCtrlBytes)) != ADAMAS_OK) return rc;
   p.err = err_word(a.workspace);
-  const dim3 grid((unsigned)((p.geo.Nmax + 127) / 128), (unsigned)(a.B * a.Hkv));
-  accumulate_chunk_rows_kernel<<<grid, 128, 0, (cudaStream_t)stream>>>(p);
+  int sms = 0;
+  if ((rc = attend_device(&sms)) != ADAMAS_OK) return rc;
+  const int64_t rows = cache_rows(a, p.geo);
+  const int64_t units = (int64_t)a.B * a.Hkv * ((p.geo.Nmax + 255) / 256);
+  if (rows > INT32_MAX || units > INT32_MAX) return ADAMAS_ERR_UNSUPPORTED;
+  WtParams wp;
+  wp.c = p;
+  wp.TQ = 128 / p.G;
+  wp.box = rows_box(p.geo, a.page_size);
+  CUtensorMap q_map = {}, k_map = {};
+  if ((rc = query_map(a.q, a.T, a.Hq, p.G, wp.TQ, &q_map)) != ADAMAS_OK) return rc;
+  if (wp.box && (rc = rows_map(a.K, rows, wp.box, &k_map)) != ADAMAS_OK) return rc;
+  chunk_weights_kernel<<<(unsigned)(units < sms ? units : sms), kWtThreads, kWtSmem, (cudaStream_t)stream>>>(wp, q_map,
+                                                                                                             k_map);
   return launched();
 }
 
