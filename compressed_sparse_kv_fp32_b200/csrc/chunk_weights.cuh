@@ -8,9 +8,15 @@
 // exchange between threads, and the sums come in a fixed order.  Each token's total is
 // read and written once, by one thread.
 //
-// Roles: warps 0-3 and 4-7 one token per thread of tile 0 and 1; warps 8-9 copy K and Q
-// tiles (and each column's -lse log2 e); one thread of warp 10 issues the products, two
-// S per tile, so that one is summed while the other is made.
+// A chunk of at most two Q tiles stays in shared memory over all units of its head that a
+// block does one after the other (its units are then neighbours); longer chunks stream
+// through the same two buffers, and a block's units are spread over the tokens, as the
+// first ones are seen by more rows.
+//
+// Roles: a tile has two S, and each S four warps, a token per thread (warps 0-15: a tile's
+// Q tiles go to its two S in turn, and the two sums of a token are added at the unit's
+// end); warps 16-17 copy K and Q tiles (and each column's -lse log2 e); one thread of warp
+// 18 issues the products.
 //
 // Bound by the exponentials (16 per cycle and multiprocessor) or, for short chunks, by
 // reading K.
@@ -20,7 +26,7 @@
 
 namespace adamas {
 
-constexpr int kWtThreads = 352;
+constexpr int kWtThreads = 608;
 constexpr int kWtStages = 2;  // of K (two tiles each) and of Q
 constexpr size_t kWtSmem = (2 * kWtStages + kWtStages) * kTileBytes + 1024;
 
@@ -43,7 +49,7 @@ __device__ __forceinline__ WtUnit wt_unit(const WtParams& p, const int* tab, int
     if (tab[mid] <= u) lo = mid;
     else hi = mid;
   }
-  WtUnit w;
+  WtUnit w = {};
   bool bad = false;
   w.b = lo;
   ragged_rows(p.c.cu_q, lo, p.c.T, w.first, w.n, bad);
@@ -58,14 +64,82 @@ __device__ __forceinline__ WtUnit wt_unit(const WtParams& p, const int* tab, int
   return w;
 }
 
+// What the copying warps tell the others with each K stage.
+struct WtJob {
+  int bh, T0, n, len, q0, q1;
+  int q_lo;                      // first Q tile that is loaded
+  bool resident, load, release;  // Q stays over units; is new; makes room after this one
+  bool end;                      // no unit: the block is done
+};
+
+// The units of a block, and what becomes of the Q buffers at each (followed by the copying
+// warps).
+struct WtWalk {
+  int u, last, step;   // unit numbers left: u, u + step, ... <= last
+  int key;             // head whose Q tiles are resident (-1: none)
+  uint32_t fills[2];   // of each buffer
+  WtUnit w = {};
+
+  bool resident, load, release;
+  int q_lo;            // first tile that is loaded
+
+  __device__ __forceinline__ WtWalk(const WtParams& p, const int* tab, const long long* cost, int units, bool near) {
+    const int n = gridDim.x, c = blockIdx.x;
+    u = near ? first_unit(p, tab, cost, cost[p.c.B] * c / n) : c;
+    last = (near ? first_unit(p, tab, cost, cost[p.c.B] * (c + 1) / n) : units) - 1;
+    step = near ? 1 : n;
+    key = -1;
+    fills[0] = fills[1] = 0;
+    if (u <= last) w = wt_unit(p, tab, u);
+  }
+  // The first unit that begins at or behind place x when a sequence's units take
+  // (cost[b + 1] - cost[b]) / (tab[b + 1] - tab[b]) places each.
+  static __device__ __forceinline__ int first_unit(const WtParams& p, const int* tab, const long long* cost, long long x) {
+    int lo = 0, hi = p.c.B;  // cost[lo] <= x < cost[hi], or x is the end
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cost[mid] <= x) lo = mid;
+      else hi = mid;
+    }
+    const int nu = tab[lo + 1] - tab[lo];
+    if (nu == 0) return tab[lo];
+    const long long each = (cost[lo + 1] - cost[lo]) / nu;
+    return tab[lo] + (int)((x - cost[lo] + each - 1) / each);
+  }
+  __device__ __forceinline__ bool stays(const WtUnit& x) const { return x.q1 <= 2; }
+  // prepares the unit at hand; false: none left
+  __device__ __forceinline__ bool begin(const WtParams& p, const int* tab, WtUnit& next) {
+    if (u > last) return false;
+    const int head = w.b * p.c.Hkv + w.h;
+    resident = stays(w);
+    load = !resident || head != key;
+    key = resident ? head : -1;
+    q_lo = resident ? 0 : w.q0;
+    release = true;
+    if (u + step <= last) {
+      next = wt_unit(p, tab, u + step);
+      release = !(resident && stays(next) && next.b == w.b && next.h == w.h);
+    }
+    return true;
+  }
+  __device__ __forceinline__ void end(const WtUnit& next) {
+    u += step;
+    w = next;
+  }
+};
+
 __global__ void __launch_bounds__(kWtThreads, 1)
     chunk_weights_kernel(const WtParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map) {
   extern __shared__ unsigned char smem_raw[];
-  __shared__ int tab[kMaxBatch + 1];
+  __shared__ int tab[kMaxBatch + 1];         // units before each sequence
+  __shared__ long long cost[kMaxBatch + 1];  // and what they cost: a place for K, one per Q tile
   __shared__ __align__(16) float neg_lse[kWtStages][128];
   __shared__ __align__(8) uint64_t k_full[kWtStages], k_empty[kWtStages], q_full[kWtStages], q_empty[kWtStages],
       s_full[2][2], s_empty[2][2], all_done;
+  __shared__ WtJob jobs[kWtStages];
+  __shared__ float part[2][2][128];  // sums of the second S, of even and odd units
   __shared__ uint32_t tmem_slot, gave_up;
+  __shared__ int longest;  // chunk of the batch
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t k_ring = base, q_ring = base + 2 * kWtStages * kTileBytes;
@@ -73,9 +147,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kWtStages; ++i) {
       mbar_init(&k_full[i], 64);
-      mbar_init(&k_empty[i], 1);
+      mbar_init(&k_empty[i], 1 + 16);  // the products and the readers of the job
       mbar_init(&q_full[i], 64);
-      mbar_init(&q_empty[i], 1 + 8);  // the products and the readers of neg_lse
+      mbar_init(&q_empty[i], 1 + 16);  // the products and the readers of neg_lse
     }
     for (int t = 0; t < 2; ++t)
       for (int i = 0; i < 2; ++i) {
@@ -86,11 +160,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     gave_up = 0;
     fence_mbar_init();
   }
-  if (warp == 10) tmem_alloc512(&tmem_slot);
+  if (warp == 18) tmem_alloc512(&tmem_slot);
   if (warp == 0) {  // units before each sequence
-    int all = 0;
+    int all = 0, most = 0;
+    long long places = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
       int s = 0;
+      long long z = 0;
       if (b0 + lane < p.c.B) {
         bool bad_cu = false, bad_len = false;
         int first, n;
@@ -99,17 +175,33 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         if (bad_cu) atomicOr(p.c.err, kErrOffsets);
         if (bad_len) atomicOr(p.c.err, kErrSeqLen);
         if (n > 0) s = (len + 255) / 256 * p.c.Hkv;
+        z = (long long)s * (1 + (n + p.TQ - 1) / p.TQ);
+        most = n > most ? n : most;
       }
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, s, d);
-        if (lane >= d) s += u;
+        const long long y = __shfl_up_sync(0xffffffffu, z, d);
+        if (lane >= d) {
+          s += u;
+          z += y;
+        }
       }
       s += all;
-      if (b0 + lane < p.c.B) tab[b0 + lane + 1] = s;
+      z += places;
+      if (b0 + lane < p.c.B) {
+        tab[b0 + lane + 1] = s;
+        cost[b0 + lane + 1] = z;
+      }
       all = __shfl_sync(0xffffffffu, s, 31);
+      places = __shfl_sync(0xffffffffu, z, 31);
     }
-    if (lane == 0) tab[0] = 0;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      tab[0] = 0;
+      cost[0] = 0;
+      longest = most;
+    }
   }
   tmem_fence_before();
   __syncthreads();
@@ -117,85 +209,121 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   const uint32_t tmem = tmem_slot;  // columns: tile 0's two S, tile 1's two S, 128 each
   const int units = tab[p.c.B];
 
-  if (warp < 8) {
+  if (warp < 16) {
     // ------------------------------------------------------------ sums of weights
-    const int t = warp >> 2, r = (warp & 3) * 32 + lane, G = p.c.G;
-    const uint32_t S = tmem + ((uint32_t)(warp & 3) << 21) + 256 * t;
-    uint32_t is = 0, iq = 0;  // S of this tile, Q tiles
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-      const WtUnit w = wt_unit(p, tab, u);
+    const int t = (warp >> 2) & 1, buf = warp >> 3, r = (warp & 3) * 32 + lane, G = p.c.G;
+    const uint32_t from = tmem + ((uint32_t)(warp & 3) << 21) + 256 * t + 128 * buf;
+    uint32_t is = 0, fills[2] = {0, 0};  // S of this tile, fills of the Q buffers
+    for (uint32_t ik = 0;; ++ik) {
+      const uint32_t ks = ik % kWtStages;
+      mbar_wait_or_give_up(&k_full[ks], (ik / kWtStages) & 1, &gave_up);
+      const WtJob w = jobs[ks];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_empty[ks]);
+      if (w.end || *(volatile uint32_t*)&gave_up) break;
       const int slot = w.T0 + 128 * t + r;
       const bool tile = w.T0 + 128 * t < w.len;
-      float* out = p.c.mass + ((int64_t)w.b * p.c.Hkv + w.h) * p.c.geo.Nmax + slot;
+      float* out = p.c.mass + (int64_t)w.bh * p.c.geo.Nmax + slot;
       float before = 0.0f;
-      if (slot < w.len) before = *out;
-      uint64_t sum[2] = {0, 0};
-      for (int q = w.q0; q < w.q1; ++q, ++iq) {
-        const uint32_t stage = iq % kWtStages;
-        mbar_wait_or_give_up(&q_full[stage], (iq / kWtStages) & 1, &gave_up);  // neg_lse is there
-        if (tile) {
-          mbar_wait_or_give_up(&s_full[t][is & 1], (is >> 1) & 1, &gave_up);
+      if (buf == 0 && slot < w.len) before = *out;
+      uint64_t sum[4] = {0, 0, 0, 0};
+      if (w.load && w.resident) {
+        ++fills[0];
+        if (w.q1 > 1) ++fills[1];
+      }
+      for (int q = w.q0; q < w.q1; ++q) {
+        const uint32_t stage = (q - w.q_lo) & 1;
+        if (!w.resident) ++fills[stage];
+        mbar_wait_or_give_up(&q_full[stage], (fills[stage] - 1) & 1, &gave_up);  // neg_lse is there
+        if (tile && (is++ & 1) == (uint32_t)buf) {
+          mbar_wait_or_give_up(&s_full[t][buf], ((is - 1) >> 1) & 1, &gave_up);
           tmem_fence_after();
           // the columns that see the slot: those of the tokens at or behind it
           const int tok0 = q * p.TQ, toks = w.n - tok0 < p.TQ ? w.n - tok0 : p.TQ;
           const int c1 = toks * G;
           int c0 = (slot - (w.len - w.n) - tok0) * G;
           c0 = slot >= w.len ? 128 : (c0 < 0 ? 0 : c0);
-          const bool edge = __any_sync(0xffffffffu, c0 > 0) || c1 < 128;
-          const uint32_t from = S + 128 * (is & 1);
-          uint32_t x[4][32];
-          tmem_ld32(from, x[0]);
-          tmem_ld32(from + 32, x[1]);
-          tmem_ld32(from + 64, x[2]);
-          tmem_ld32(from + 96, x[3]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_wait_ld(x[c]);
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[t][is & 1]);
+          const bool some = __any_sync(0xffffffffu, c0 > 0);
           const uint64_t scale2 = f2_pack(kScoreLog2, kScoreLog2);
           const uint32_t nl = smem_addr(&neg_lse[stage][0]);
+          // 32 columns at a time, the next ones on their way meanwhile
+          uint32_t xa[32], xb[32];
+          auto add = [&](uint32_t (&x)[32], int i0) {
+            if (i0 >= c1) return;
+            if (some || i0 + 32 > c1) {  // columns that do not see the slot: a score of -inf
 #pragma unroll
-          for (int i = 0; i < 128; i += 4) {
-            const uint4 z = lds128(nl + 4 * i);
-            const uint64_t e0 = f2_fma(f2_pack(__uint_as_float(x[i >> 5][i & 31]), __uint_as_float(x[i >> 5][(i & 31) + 1])),
-                                       scale2, f2_pack(__uint_as_float(z.x), __uint_as_float(z.y)));
-            const uint64_t e1 = f2_fma(f2_pack(__uint_as_float(x[i >> 5][(i & 31) + 2]), __uint_as_float(x[i >> 5][(i & 31) + 3])),
-                                       scale2, f2_pack(__uint_as_float(z.z), __uint_as_float(z.w)));
-            float a, b, c, d;
-            f2_unpack(e0, a, b);
-            f2_unpack(e1, c, d);
-            a = fast_exp2(a);
-            b = fast_exp2(b);
-            c = fast_exp2(c);
-            d = fast_exp2(d);
-            if (edge) {
-              a = i >= c0 && i < c1 ? a : 0.0f;
-              b = i + 1 >= c0 && i + 1 < c1 ? b : 0.0f;
-              c = i + 2 >= c0 && i + 2 < c1 ? c : 0.0f;
-              d = i + 3 >= c0 && i + 3 < c1 ? d : 0.0f;
+              for (int i = 0; i < 32; ++i) x[i] = i0 + i >= c0 && i0 + i < c1 ? x[i] : 0xFF800000u;
             }
-            sum[0] = f2_add(sum[0], f2_pack(a, b));
-            sum[1] = f2_add(sum[1], f2_pack(c, d));
-          }
-          ++is;
+#pragma unroll
+            for (int hf = 0; hf < 32; hf += 16) {
+              uint4 z[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) z[i] = lds128(nl + 4 * (i0 + hf) + 16 * i);
+              float e[16];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int n = hf + 4 * i;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[n]), __uint_as_float(x[n + 1])), scale2,
+                                 f2_pack(__uint_as_float(z[i].x), __uint_as_float(z[i].y))),
+                          e[4 * i], e[4 * i + 1]);
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[n + 2]), __uint_as_float(x[n + 3])), scale2,
+                                 f2_pack(__uint_as_float(z[i].z), __uint_as_float(z[i].w))),
+                          e[4 * i + 2], e[4 * i + 3]);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) e[i] = fast_exp2(e[i]);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) sum[i & 3] = f2_add(sum[i & 3], f2_pack(e[2 * i], e[2 * i + 1]));
+            }
+          };
+          tmem_ld32(from, xa);
+          tmem_wait_ld(xa);
+          tmem_ld32(from + 32, xb);
+          add(xa, 0);
+          tmem_wait_ld(xb);
+          tmem_ld32(from + 64, xa);
+          add(xb, 32);
+          tmem_wait_ld(xa);
+          tmem_ld32(from + 96, xb);
+          add(xa, 64);
+          tmem_wait_ld(xb);
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[t][buf]);
+          add(xb, 96);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_empty[stage]);
+        if (!w.resident) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_empty[stage]);
+        }
       }
-      if (slot < w.len) {
-        float a, b;
-        f2_unpack(f2_add(sum[0], sum[1]), a, b);
-        *out = before + (a + b);
+      float a, b;
+      f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
+      // the tile's two sums meet; the next but one unit's take their place, a barrier later
+      if (buf == 1) part[ik & 1][t][r] = a + b;
+      named_sync(1 + t, 256);
+      if (buf == 0 && slot < w.len) *out = before + ((a + b) + part[ik & 1][t][r]);
+      if (w.resident && w.release) {
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&q_empty[0]);
+          if (w.q1 > 1) mbar_arrive(&q_empty[1]);
+        }
       }
     }
-  } else if (warp < 10) {
+  } else if (warp < 18) {
     // ------------------------------------------------------------ copies
-    const int lt = tid - 256, lr = lt >> 4, lc = lt & 15;
-    uint32_t ik = 0, iq = 0;
+    const int lt = tid - 512, lr = lt >> 4, lc = lt & 15;
+    WtWalk k = WtWalk(p, tab, cost, units, longest <= 2 * p.TQ);
+    WtUnit next;
+    uint32_t ik = 0;
     bool bad = false;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++ik) {
-      const WtUnit w = wt_unit(p, tab, u);
+    auto publish = [&](uint32_t stage, bool end) {  // by the thread that arrives first
+      const WtUnit& w = k.w;
+      jobs[stage] = WtJob{w.b * p.c.Hkv + w.h, w.T0, w.n, w.len, w.q0, w.q1, k.q_lo, k.resident, k.load, k.release, end};
+    };
+    for (; k.begin(p, tab, next); ++ik) {
+      const WtUnit& w = k.w;
       const uint32_t stage = ik % kWtStages, dst = k_ring + 2 * stage * kTileBytes;
       const int rows = w.len - w.T0 < 256 ? w.len - w.T0 : 256;
       if (p.box) {
@@ -203,7 +331,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         uint32_t row = 0;
         if (lt < pieces) row = p.c.geo.row32(w.b, w.h, w.T0 + lt * p.box, bad);
         mbar_wait_or_give_up(&k_empty[stage], ((ik / kWtStages) & 1) ^ 1, &gave_up);
-        if (lt == 0) mbar_arrive_expect_tx(&k_full[stage], (uint32_t)(pieces * p.box * 2 * kDim));
+        if (lt == 0) {
+          publish(stage, false);
+          mbar_arrive_expect_tx(&k_full[stage], (uint32_t)(pieces * p.box * 2 * kDim));
+        }
         if (lt < 32) {
           __syncwarp();
           if (lt < pieces) {
@@ -216,6 +347,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         if (lt != 0) mbar_arrive(&k_full[stage]);
       } else {
         mbar_wait_or_give_up(&k_empty[stage], ((ik / kWtStages) & 1) ^ 1, &gave_up);
+        if (lt == 0) publish(stage, false);
 #pragma unroll 4
         for (int r = lr; r < rows; r += 4) {
           const uint32_t row = p.c.geo.row32(w.b, w.h, w.T0 + r, bad);
@@ -223,8 +355,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
         cp_async_arrive(&k_full[stage]);
       }
-      for (int q = w.q0; q < w.q1; ++q, ++iq) {
-        const uint32_t qs = iq % kWtStages;
+      for (int q = k.q_lo; q < w.q1 && k.load; ++q) {
+        const uint32_t qs = (q - k.q_lo) & 1;
         const int tok0 = q * p.TQ, cols = (w.n - tok0 < p.TQ ? w.n - tok0 : p.TQ) * p.c.G;
         float z[2];
 #pragma unroll
@@ -236,7 +368,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (v != -INFINITY) z[j] = -v * 1.4426950408889634f;
           }
         }
-        mbar_wait_or_give_up(&q_empty[qs], ((iq / kWtStages) & 1) ^ 1, &gave_up);
+        mbar_wait_or_give_up(&q_empty[qs], (k.fills[qs]++ & 1) ^ 1, &gave_up);
         neg_lse[qs][lt] = z[0];
         neg_lse[qs][lt + 64] = z[1];
         if (lt == 0) {
@@ -247,31 +379,45 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           mbar_arrive(&q_full[qs]);
         }
       }
+      k.end(next);
     }
+    mbar_wait_or_give_up(&k_empty[ik % kWtStages], ((ik / kWtStages) & 1) ^ 1, &gave_up);
+    if (lt == 0) publish(ik % kWtStages, true);
+    mbar_arrive(&k_full[ik % kWtStages]);
     cp_async_wait<0>();
     if (bad) atomicOr(p.c.err, kErrTable);
   } else if (lane == 0) {
     // ------------------------------------------------------------ products
-    uint32_t ik = 0, iq = 0, is[2] = {0, 0};
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++ik) {
-      const WtUnit w = wt_unit(p, tab, u);
-      const uint32_t stage = ik % kWtStages, k = k_ring + 2 * stage * kTileBytes;
-      const int nt = w.T0 + 128 < w.len ? 2 : 1;
+    uint32_t is[2] = {0, 0}, fills[2] = {0, 0};
+    for (uint32_t ik = 0;; ++ik) {
+      const uint32_t stage = ik % kWtStages, kt = k_ring + 2 * stage * kTileBytes;
       mbar_wait_or_give_up(&k_full[stage], (ik / kWtStages) & 1, &gave_up);
+      const WtJob w = jobs[stage];
+      if (w.end || *(volatile uint32_t*)&gave_up) break;
       if (!p.box) fence_async_smem();
-      for (int q = w.q0; q < w.q1; ++q, ++iq) {
-        const uint32_t qs = iq % kWtStages;
-        mbar_wait_or_give_up(&q_full[qs], (iq / kWtStages) & 1, &gave_up);
+      const int nt = w.T0 + 128 < w.len ? 2 : 1;
+      if (w.load && w.resident) {
+        ++fills[0];
+        if (w.q1 > 1) ++fills[1];
+      }
+      for (int q = w.q0; q < w.q1; ++q) {
+        const uint32_t qs = (q - w.q_lo) & 1;
+        if (!w.resident) ++fills[qs];
+        mbar_wait_or_give_up(&q_full[qs], (fills[qs] - 1) & 1, &gave_up);
         for (int t = 0; t < nt; ++t) {
           mbar_wait_or_give_up(&s_empty[t][is[t] & 1], ((is[t] >> 1) & 1) ^ 1, &gave_up);
           tmem_fence_after();
-          mma_rows_rows(tmem + 256 * t + 128 * (is[t] & 1), k + t * kTileBytes, q_ring + qs * kTileBytes);
+          mma_rows_rows(tmem + 256 * t + 128 * (is[t] & 1), kt + t * kTileBytes, q_ring + qs * kTileBytes);
           mma_commit(&s_full[t][is[t] & 1]);
           ++is[t];
         }
-        mma_commit(&q_empty[qs]);
+        if (!w.resident) mma_commit(&q_empty[qs]);
       }
       mma_commit(&k_empty[stage]);
+      if (w.resident && w.release) {
+        mma_commit(&q_empty[0]);
+        if (w.q1 > 1) mma_commit(&q_empty[1]);
+      }
     }
     mma_commit(&all_done);
     mbar_wait_or_give_up(&all_done, 0, &gave_up);
@@ -280,7 +426,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  if (warp == 10) tmem_free512(tmem);
+  if (warp == 18) tmem_free512(tmem);
   if (tid == 0 && gave_up) atomicOr(p.c.err, kErrTimeout);
 }
 
