@@ -13,10 +13,10 @@
 // through the same two buffers, and a block's units are spread over the tokens, as the
 // first ones are seen by more rows.
 //
-// Roles: a tile has two S, and each S four warps, a token per thread (warps 0-15: a tile's
-// Q tiles go to its two S in turn, and the two sums of a token are added at the unit's
-// end); warps 16-17 copy K and Q tiles (and each column's -lse log2 e); one thread of warp
-// 18 issues the products.
+// Roles: warps 0-7 and 8-15 one token per thread of even and of odd units, which are at
+// work at the same time (one unit's waits and ends lie in the other one's exponentials);
+// warps 16-17 copy K and Q tiles (and each column's -lse log2 e); one thread of warp 18
+// issues the products of even units, one of warp 19 those of odd ones.
 //
 // Bound by the exponentials (16 per cycle and multiprocessor) or, for short chunks, by
 // reading K.
@@ -26,7 +26,7 @@
 
 namespace adamas {
 
-constexpr int kWtThreads = 608;
+constexpr int kWtThreads = 640;
 constexpr int kWtStages = 2;  // of K (two tiles each) and of Q
 constexpr size_t kWtSmem = (2 * kWtStages + kWtStages) * kTileBytes + 1024;
 
@@ -137,7 +137,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   __shared__ __align__(8) uint64_t k_full[kWtStages], k_empty[kWtStages], q_full[kWtStages], q_empty[kWtStages],
       s_full[2][2], s_empty[2][2], all_done;
   __shared__ WtJob jobs[kWtStages];
-  __shared__ float part[2][2][128];  // sums of the second S, of even and odd units
   __shared__ uint32_t tmem_slot, gave_up;
   __shared__ int longest;  // chunk of the batch
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -147,16 +146,16 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kWtStages; ++i) {
       mbar_init(&k_full[i], 64);
-      mbar_init(&k_empty[i], 1 + 16);  // the products and the readers of the job
+      mbar_init(&k_empty[i], 2 + 16);  // the products and the readers of the job
       mbar_init(&q_full[i], 64);
-      mbar_init(&q_empty[i], 1 + 16);  // the products and the readers of neg_lse
+      mbar_init(&q_empty[i], 2 + 16);  // the products and the readers of neg_lse
     }
     for (int t = 0; t < 2; ++t)
       for (int i = 0; i < 2; ++i) {
         mbar_init(&s_full[t][i], 1);
         mbar_init(&s_empty[t][i], 4);
       }
-    mbar_init(&all_done, 1);
+    mbar_init(&all_done, 2);
     gave_up = 0;
     fence_mbar_init();
   }
@@ -213,7 +212,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     // ------------------------------------------------------------ sums of weights
     const int t = (warp >> 2) & 1, buf = warp >> 3, r = (warp & 3) * 32 + lane, G = p.c.G;
     const uint32_t from = tmem + ((uint32_t)(warp & 3) << 21) + 256 * t + 128 * buf;
-    uint32_t is = 0, fills[2] = {0, 0};  // S of this tile, fills of the Q buffers
+    uint32_t is = 0, fills[2] = {0, 0};  // S taken, fills of the Q buffers
     for (uint32_t ik = 0;; ++ik) {
       const uint32_t ks = ik % kWtStages;
       mbar_wait_or_give_up(&k_full[ks], (ik / kWtStages) & 1, &gave_up);
@@ -221,11 +220,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_empty[ks]);
       if (w.end || *(volatile uint32_t*)&gave_up) break;
+      const bool mine = ks == (uint32_t)buf;
       const int slot = w.T0 + 128 * t + r;
-      const bool tile = w.T0 + 128 * t < w.len;
+      const bool tile = mine && w.T0 + 128 * t < w.len;
       float* out = p.c.mass + (int64_t)w.bh * p.c.geo.Nmax + slot;
       float before = 0.0f;
-      if (buf == 0 && slot < w.len) before = *out;
+      if (mine && slot < w.len) before = *out;
       uint64_t sum[4] = {0, 0, 0, 0};
       if (w.load && w.resident) {
         ++fills[0];
@@ -234,9 +234,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       for (int q = w.q0; q < w.q1; ++q) {
         const uint32_t stage = (q - w.q_lo) & 1;
         if (!w.resident) ++fills[stage];
-        mbar_wait_or_give_up(&q_full[stage], (fills[stage] - 1) & 1, &gave_up);  // neg_lse is there
-        if (tile && (is++ & 1) == (uint32_t)buf) {
-          mbar_wait_or_give_up(&s_full[t][buf], ((is - 1) >> 1) & 1, &gave_up);
+        if (mine || !w.resident)  // neg_lse is there
+          mbar_wait_or_give_up(&q_full[stage], (fills[stage] - 1) & 1, &gave_up);
+        if (tile) {
+          mbar_wait_or_give_up(&s_full[t][buf], is++ & 1, &gave_up);
           tmem_fence_after();
           // the columns that see the slot: those of the tokens at or behind it
           const int tok0 = q * p.TQ, toks = w.n - tok0 < p.TQ ? w.n - tok0 : p.TQ;
@@ -297,12 +298,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           if (lane == 0) mbar_arrive(&q_empty[stage]);
         }
       }
-      float a, b;
-      f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
-      // the tile's two sums meet; the next but one unit's take their place, a barrier later
-      if (buf == 1) part[ik & 1][t][r] = a + b;
-      named_sync(1 + t, 256);
-      if (buf == 0 && slot < w.len) *out = before + ((a + b) + part[ik & 1][t][r]);
+      if (mine && slot < w.len) {
+        float a, b;
+        f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
+        *out = before + (a + b);
+      }
       if (w.resident && w.release) {
         __syncwarp();
         if (lane == 0) {
@@ -388,33 +388,39 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     if (bad) atomicOr(p.c.err, kErrTable);
   } else if (lane == 0) {
     // ------------------------------------------------------------ products
-    uint32_t is[2] = {0, 0}, fills[2] = {0, 0};
+    const uint32_t buf = warp - 18;
+    uint32_t made[2] = {0, 0}, fills[2] = {0, 0};  // S of each tile, fills of the Q buffers
     for (uint32_t ik = 0;; ++ik) {
       const uint32_t stage = ik % kWtStages, kt = k_ring + 2 * stage * kTileBytes;
       mbar_wait_or_give_up(&k_full[stage], (ik / kWtStages) & 1, &gave_up);
       const WtJob w = jobs[stage];
       if (w.end || *(volatile uint32_t*)&gave_up) break;
+      const bool mine = stage == buf;
+      if (!mine) mbar_arrive(&k_empty[stage]);
       if (!p.box) fence_async_smem();
       const int nt = w.T0 + 128 < w.len ? 2 : 1;
       if (w.load && w.resident) {
         ++fills[0];
         if (w.q1 > 1) ++fills[1];
       }
-      for (int q = w.q0; q < w.q1; ++q) {
+      for (int q = w.q0; q < w.q1 && (mine || !w.resident); ++q) {
         const uint32_t qs = (q - w.q_lo) & 1;
         if (!w.resident) ++fills[qs];
         mbar_wait_or_give_up(&q_full[qs], (fills[qs] - 1) & 1, &gave_up);
+        if (!mine) {
+          mbar_arrive(&q_empty[qs]);
+          continue;
+        }
         for (int t = 0; t < nt; ++t) {
-          mbar_wait_or_give_up(&s_empty[t][is[t] & 1], ((is[t] >> 1) & 1) ^ 1, &gave_up);
+          mbar_wait_or_give_up(&s_empty[t][buf], (made[t]++ & 1) ^ 1, &gave_up);
           tmem_fence_after();
-          mma_rows_rows(tmem + 256 * t + 128 * (is[t] & 1), kt + t * kTileBytes, q_ring + qs * kTileBytes);
-          mma_commit(&s_full[t][is[t] & 1]);
-          ++is[t];
+          mma_rows_rows(tmem + 256 * t + 128 * buf, kt + t * kTileBytes, q_ring + qs * kTileBytes);
+          mma_commit(&s_full[t][buf]);
         }
         if (!w.resident) mma_commit(&q_empty[qs]);
       }
-      mma_commit(&k_empty[stage]);
-      if (w.resident && w.release) {
+      if (mine) mma_commit(&k_empty[stage]);
+      if (w.resident && w.release) {  // (what the thread issued for units before is done then, too)
         mma_commit(&q_empty[0]);
         if (w.q1 > 1) mma_commit(&q_empty[1]);
       }
