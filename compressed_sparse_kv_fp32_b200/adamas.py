@@ -175,8 +175,10 @@ def _check(rc: int, where: str):
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle alone: making a Stream object for it takes 3 us
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -515,17 +517,17 @@ def rope_frequencies(rot_dim: int = HEAD_DIM, base: float = 10000.0, *, scaling:
     return torch.tensor(turns, dtype=torch.int64, device=device if device is not None else "cuda"), mscale
 
 
-def _on(device: torch.device, t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple):
-    """An argument of a cache operator: on `device`, dense, of this type and shape; its
-    address (None for None)."""
+def _on(dev: int, t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple):
+    """An argument of a cache operator: on CUDA device `dev`, dense, of this type and
+    shape; its address (None for None).  (A call checks about ten of them.)"""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
@@ -533,16 +535,23 @@ def _on(device: torch.device, t: Optional[torch.Tensor], name: str, dtype: torch
     return t.data_ptr()
 
 
-def _device_of(t: torch.Tensor, name: str) -> torch.device:
+def _device_of(t: torch.Tensor, name: str) -> int:
     """The device of a call: that of its first tensor, which must be the current one
     (the launch goes to the current device's stream)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
+    return dev
+
+
+def _run(name: str, args: ctypes.Structure, stream: Optional[torch.cuda.Stream]):
+    rc = getattr(_lib if _lib is not None else load(), name)(ctypes.byref(args), _stream(stream))
+    if rc != 0:
+        raise AdamasError(rc, name)
 
 
 def _cache_of(dev, K, V, codes, B, block_table, suffix=""):
@@ -573,15 +582,15 @@ def _packed_rows(dev, x: Optional[torch.Tensor], name: str):
         raise TypeError(f"{name} must be a torch.Tensor")
     if x.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
-    if x.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {x.device}")
+    if x.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {x.device}")
     if x.dim() != 3 or x.shape[2] != HEAD_DIM:
         raise ValueError(f"{name} must be [T, heads, 128]")
     T, H, d = x.shape
-    if T and (x.stride(2) != 1 or (H > 1 and x.stride(1) != d)):
+    row, head, one = x.stride()
+    if T and (one != 1 or (H > 1 and head != d)):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    stride = x.stride(0) if T > 1 else max(H * d, x.stride(0) // 8 * 8)
-    return T, H, stride, x.data_ptr()
+    return T, H, row if T > 1 else max(H * d, row // 8 * 8), x.data_ptr()
 
 
 def rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],
@@ -620,14 +629,14 @@ def rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optiona
         if out is not None:
             raise ValueError("out without q")
     elif out is None:
-        out = torch.zeros((T, Hq, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        out = torch.zeros((T, Hq, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
     a = RopeArgs(pq, pk, pv, sq, sk, sv, _on(dev, cu_new, "cu_new", torch.int32, (B + 1,)),
                  _on(dev, cache_lens, "cache_lens", torch.int32, (B,)),
                  _on(dev, positions, "positions", torch.int32, (T,)),
                  _on(dev, freqs, "freqs", torch.int64, freqs.shape), 2 * freqs.shape[0], int(interleaved), mscale,
                  T, B, Hq or Hkv, Hkv, Nmax, HEAD_DIM, _on(dev, out, "out", torch.bfloat16, (T, Hq, HEAD_DIM)),
                  *ptrs, *paged, workspace.buffer.data_ptr(), workspace.nbytes)
-    _check(load().adamas_rope_append(ctypes.byref(a), _stream(stream)), "adamas_rope_append")
+    _run("adamas_rope_append", a, stream)
     return out
 
 
@@ -659,13 +668,13 @@ def chunk_attend(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.
     head, paged = _chunk_args(dev, q, K, V, cu_q, seq_lens, block_table)
     T, Hq = head[5], head[7]
     if out is None:
-        out = torch.zeros((T, Hq, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        out = torch.zeros((T, Hq, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.zeros((T, Hq), dtype=torch.float32, device=dev)
+        lse = torch.zeros((T, Hq), dtype=torch.float32, device=q.device)
     a = ChunkArgs(*head, _on(dev, out, "out", torch.bfloat16, (T, Hq, HEAD_DIM)),
                   _on(dev, lse, "lse", torch.float32, (T, Hq)), None, *paged, workspace.buffer.data_ptr(),
                   workspace.nbytes)
-    _check(load().adamas_chunk_attend(ctypes.byref(a), _stream(stream)), "adamas_chunk_attend")
+    _run("adamas_chunk_attend", a, stream)
     return out, lse
 
 
@@ -681,7 +690,7 @@ def accumulate_chunk(q: torch.Tensor, K: torch.Tensor, lse: torch.Tensor, cu_q: 
     a = ChunkArgs(*head, None, _on(dev, lse, "lse", torch.float32, (T, Hq)),
                   _on(dev, mass, "mass", torch.float32, (B, Hkv, Nmax)), *paged, workspace.buffer.data_ptr(),
                   workspace.nbytes)
-    _check(load().adamas_accumulate_chunk(ctypes.byref(a), _stream(stream)), "adamas_accumulate_chunk")
+    _run("adamas_accumulate_chunk", a, stream)
     return mass
 
 
@@ -706,7 +715,7 @@ def accumulate_kept(q: torch.Tensor, K: torch.Tensor, idx: torch.Tensor, seq_len
                  _on(dev, seq_lens, "seq_lens", torch.int32, (B,)), B, Hq, Hkv, Nmax, HEAD_DIM, budget, policy,
                  _on(dev, mass, "mass", torch.float32, (B, Hkv, Nmax)), *paged, workspace.buffer.data_ptr(),
                  workspace.nbytes)
-    _check(load().adamas_accumulate_kept(ctypes.byref(a), _stream(stream)), "adamas_accumulate_kept")
+    _run("adamas_accumulate_kept", a, stream)
     return mass
 
 
@@ -739,14 +748,14 @@ def evict(K: torch.Tensor, V: torch.Tensor, mass: torch.Tensor, seq_lens: torch.
         if Hkv_out != Hkv:
             raise ValueError(f"K_out must have {Hkv} kv heads, got {Hkv_out}")
     if kept is None:
-        kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=dev)
+        kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=K.device)
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        new_lens = torch.empty((B,), dtype=torch.int32, device=K.device)
     a = EvictArgs(*ptrs, _on(dev, mass, "mass", torch.float32, (B, Hkv, Nmax)),
                   _on(dev, seq_lens, "seq_lens", torch.int32, (B,)), B, Hkv, Nmax, HEAD_DIM, keep, n_sink, n_recent,
                   _on(dev, kept, "kept", torch.int32, (B, Hkv, max(keep, 0))),
                   _on(dev, new_lens, "new_lens", torch.int32, (B,)), *paged, *ptrs_out,
                   _on(dev, mass_out, "mass_out", torch.float32, (B, Hkv, Nmax_out)), Nmax_out, *paged_out,
                   workspace.buffer.data_ptr(), workspace.nbytes)
-    _check(load().adamas_evict(ctypes.byref(a), _stream(stream)), "adamas_evict")
+    _run("adamas_evict", a, stream)
     return kept, new_lens
