@@ -303,7 +303,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
         *out = before + (a + b);
       }
-      if (w.resident && w.release) {
+      if (w.resident && w.release) {  // not before the buffers were filled: this may be the unit they are for
+        mbar_wait_or_give_up(&q_full[0], (fills[0] - 1) & 1, &gave_up);
+        if (w.q1 > 1) mbar_wait_or_give_up(&q_full[1], (fills[1] - 1) & 1, &gave_up);
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&q_empty[0]);
@@ -421,6 +423,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       }
       if (mine) mma_commit(&k_empty[stage]);
       if (w.resident && w.release) {  // (what the thread issued for units before is done then, too)
+        mbar_wait_or_give_up(&q_full[0], (fills[0] - 1) & 1, &gave_up);
+        if (w.q1 > 1) mbar_wait_or_give_up(&q_full[1], (fills[1] - 1) & 1, &gave_up);
         mma_commit(&q_empty[0]);
         if (w.q1 > 1) mma_commit(&q_empty[1]);
       }

@@ -182,6 +182,10 @@ ATTEND = [
     (2, 2, [257], [513], 513, 0, 0, 0),
     (24, 8, [1, 9, 2], [700, 350, 512], 704, 16, 0, 0),
     (8, 2, [300, 1], [2000, 2300], 2304, 16, 0, 0),
+    # many short sequences: blocks go from head to head, with one to three units of each
+    (8, 8, [1 + i % 3 for i in range(60)], [1 + (i * 397) % 760 for i in range(60)], 768, 16, 0, 0),
+    (16, 8, [1 + (i * 7) % 150 for i in range(24)], [150 + (i * 397) % 600 for i in range(24)], 768, 0, 0, 2),
+    (8, 1, [32, 33, 1, 64, 65] * 8, [600, 70, 300, 520, 257] * 8, 640, 32, 0, 0),
 ]
 
 
