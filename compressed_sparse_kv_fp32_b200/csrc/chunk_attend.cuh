@@ -648,35 +648,54 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if (two) scores(1, 1);
             k_next();
           }
-          for (int j = 0; j < n; ++j) {
-            // what the next products wait for, asked for at once: each answer takes some 150
-            // cycles, in which the tensor cores have nothing to do
-            const bool more = j + ahead < n;
-            const bool v_in = mbar_try(&v_full[iv % kAtStages], (iv / kAtStages) & 1);
-            const bool k_in = two && more && mbar_try(&k_full[ik % kAtStages], (ik / kAtStages) & 1);
-            const bool p_in = mbar_try(&p_full[two ? 0 : j & 1], p_par[two ? 0 : j & 1]);
-            if (!v_in) mbar_wait_or_give_up(&v_full[iv % kAtStages], (iv / kAtStages) & 1, &gave_up);
-            if (!p.box) fence_async_smem();
-            if (two) {
-              if (more && !k_in) k_wait();
-              else if (!p.box) fence_async_smem();
-              for (int t = 0; t < 2; ++t) {
-                outputs(t, j > 0, t == 0 && p_in);
-                if (more) scores(t, t);
-                else mma_commit(&o_full[t]);
+          if (two) {
+            // A question to a barrier takes some 150 cycles and a commit 90, in which the tensor
+            // cores go through what was issued (about three products of sixteen columns) and then
+            // idle; so the questions for the next products are asked, and the buffers of the last
+            // ones given back, between two products of the same tile.
+            bool v_in = mbar_try(&v_full[iv % kAtStages], (iv / kAtStages) & 1);
+            bool k_in = n > 1 && mbar_try(&k_full[ik % kAtStages], (ik / kAtStages) & 1);
+            for (int j = 0; j < n; ++j) {
+              const bool more = j + 1 < n;
+              if (!v_in) mbar_wait_or_give_up(&v_full[iv % kAtStages], (iv / kAtStages) & 1, &gave_up);
+              if (more && !k_in) mbar_wait_or_give_up(&k_full[ik % kAtStages], (ik / kAtStages) & 1, &gave_up);
+              if (!p.box) fence_async_smem();
+              outputs(0, j > 0, false);
+              if (j > 0) {  // the buffers of the tiles before (their products precede this one)
+                mma_commit(&v_empty[(iv - 1) % kAtStages]);
+                mma_commit(&k_empty[(ik - 1) % kAtStages]);
               }
-              mma_commit(&v_empty[iv++ % kAtStages]);
-              if (more) k_next();
-              if (j + ahead + 1 == n) mma_commit(&q_empty);  // Q was read for the last time
-            } else {
+              const bool p_in = mbar_try(&p_full[1], p_par[1]);
+              if (more) scores(0, 0);
+              else mma_commit(&o_full[0]);
+              outputs(1, j > 0, p_in);
+              if (more) {
+                v_in = mbar_try(&v_full[(iv + 1) % kAtStages], ((iv + 1) / kAtStages) & 1);
+                k_in = j + 2 < n && mbar_try(&k_full[(ik + 1) % kAtStages], ((ik + 1) / kAtStages) & 1);
+                scores(1, 1);
+                if (j + 2 == n) mma_commit(&q_empty);  // Q was read for the last time
+                ++ik;
+              } else {
+                mma_commit(&o_full[1]);
+                mma_commit(&v_empty[iv % kAtStages]);
+              }
+              ++iv;
+            }
+          } else {
+            for (int j = 0; j < n; ++j) {
+              const bool more = j + 2 < n;
               const int t = j & 1;
+              const bool v_in = mbar_try(&v_full[iv % kAtStages], (iv / kAtStages) & 1);
+              const bool p_in = mbar_try(&p_full[t], p_par[t]);
+              if (!v_in) mbar_wait_or_give_up(&v_full[iv % kAtStages], (iv / kAtStages) & 1, &gave_up);
+              if (!p.box) fence_async_smem();
               outputs(t, j > 1, p_in);
               mma_commit(&v_empty[iv++ % kAtStages]);
               if (more) {
                 k_wait();
                 scores(t, 0);
                 k_next();
-                if (j + ahead + 1 == n) mma_commit(&q_empty);
+                if (j + 3 == n) mma_commit(&q_empty);
               } else {
                 mma_commit(&o_full[t]);
               }

@@ -5,8 +5,8 @@
 // K rows stay in shared memory while the chunk's rows pass, 128 at a time (TQ tokens'
 // heads of the group; for a short chunk from L2).  S^T = K Q^T (fp32, tensor memory) has
 // a token per row, so that a thread sums its own token's weights over the columns: no
-// exchange between threads, and the sums come in a fixed order.  Each token's total is
-// read and written once, by one thread.
+// exchange between threads, and the sums come in a fixed order.  Each token's total gets
+// one addition, by one thread.
 //
 // A chunk of at most two Q tiles stays in shared memory over all units of its head that a
 // block does one after the other (its units are then neighbours); longer chunks stream
@@ -224,8 +224,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       const int slot = w.T0 + 128 * t + r;
       const bool tile = mine && w.T0 + 128 * t < w.len;
       float* out = p.c.mass + (int64_t)w.bh * p.c.geo.Nmax + slot;
-      float before = 0.0f;
-      if (mine && slot < w.len) before = *out;
       uint64_t sum[4] = {0, 0, 0, 0};
       if (w.load && w.resident) {
         ++fills[0];
@@ -301,7 +299,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       if (mine && slot < w.len) {
         float a, b;
         f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
-        *out = before + (a + b);
+        atomicAdd(out, a + b);  // the one addition to this token: nothing to wait for
       }
       if (w.resident && w.release) {  // not before the buffers were filled: this may be the unit they are for
         mbar_wait_or_give_up(&q_full[0], (fills[0] - 1) & 1, &gave_up);
