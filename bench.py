@@ -30,7 +30,6 @@ from __future__ import annotations
 
 import argparse
 import ctypes
-import glob
 import hashlib
 import json
 import os
@@ -90,10 +89,16 @@ def metric_of(args, w):
             + (f", paged cache ({args.page_size}-token pages)" if args.page_size else ""))
 
 
+# what the decode step is built from (the cache operators' sources are not part of it)
+DECODE_SOURCES = ("adamas.cu", "common.cuh", "decode.cuh", "decode_ext.cuh", "decode_inst.cu", "decode_plain.cuh",
+                  "encode.cuh", "score.cuh")
+
+
 def source_hash() -> str:
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "compressed_sparse_kv_fp32_b200", "csrc", "*"))):
-        h.update(open(f, "rb").read())
+    for f in DECODE_SOURCES:
+        with open(os.path.join(ROOT, "compressed_sparse_kv_fp32_b200", "csrc", f), "rb") as src:
+            h.update(src.read())
     return h.hexdigest()[:16]
 
 

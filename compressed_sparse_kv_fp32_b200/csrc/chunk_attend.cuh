@@ -613,6 +613,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
       }
       cp_async_wait<0>();
+      // the copies land before the block goes, also when somebody gave up waiting for them
+      for (uint32_t k = 1; k <= kAtStages && k <= it; ++k)
+        mbar_wait_timed(&full[(it - k) % kAtStages], ((it - k) / kAtStages) & 1, 1000000000ull);
+      if (!is_v && nseg > 0) mbar_wait_timed(&q_full, (nseg - 1) & 1, 1000000000ull);
       if (bad) atomicOr(p.c.err, kErrTable);
     } else if (warp == 12) {
       // ---------------------------------------------------------- products

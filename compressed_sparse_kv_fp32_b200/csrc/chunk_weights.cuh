@@ -385,6 +385,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     if (lt == 0) publish(ik % kWtStages, true);
     mbar_arrive(&k_full[ik % kWtStages]);
     cp_async_wait<0>();
+    // the copies land before the block goes, also when somebody gave up waiting for them
+    for (uint32_t i = 0; i < kWtStages; ++i) {  // the last phase of each barrier
+      if (ik >= i) mbar_wait_timed(&k_full[(ik - i) % kWtStages], ((ik - i) / kWtStages) & 1, 1000000000ull);
+      if (k.fills[i] > 0) mbar_wait_timed(&q_full[i], (k.fills[i] - 1) & 1, 1000000000ull);
+    }
     if (bad) atomicOr(p.c.err, kErrTable);
   } else if (lane == 0) {
     // ------------------------------------------------------------ products

@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const Rope
         const int64_t slot = (int64_t)p.cache_lens[below - 1] + (r - first);
         const int pair = part * 32 + lane;
         if (pair < p.rot / 2) {
-          const int pos = p.positions ? p.positions[r] : (int)slot;
-          const uint64_t turn = p.freqs[pair] * (uint64_t)(int64_t)pos;
+          const int64_t pos = p.positions ? p.positions[r] : slot;
+          const uint64_t turn = p.freqs[pair] * (uint64_t)pos;
           double s, c;
           sincospi((double)(int64_t)turn * 0x1p-63, &s, &c);
           cs[tk][pair] = make_float2((float)(c * p.mscale), (float)(s * p.mscale));

@@ -568,3 +568,55 @@ def test_captured_calls_and_other_streams():
     torch.cuda.synchronize()
     assert same(o2, eager[0][0]) and same(l2, eager[0][1]) and same(m2, masses_[0]) and same(o1, eager[1][0])
     assert ws.device_error() == 0 and ws2.device_error() == 0
+
+
+def test_empty_cache_and_empty_batch():
+    q = torch.randn(3, 4, 128).to(torch.bfloat16).to(DEV)
+    K = torch.zeros(2, 2, 0, 128, dtype=torch.bfloat16, device=DEV)
+    ws = adamas.ChunkWorkspace(3, 2, 4, 2)
+    out, lse = adamas.chunk_attend(q, K, K, i32([0, 1, 3]), i32([0, 0]), ws)
+    assert not out.any() and (lse == -float("inf")).all() and ws.device_error() == 0
+    adamas.accumulate_chunk(q, K, lse, i32([0, 1, 3]), i32([0, 0]), torch.zeros(2, 2, 0, device=DEV), ws)
+    out, lse = adamas.chunk_attend(q[:0], K, K, i32([0, 0, 0]), i32([0, 0]), ws)
+    assert out.shape == (0, 4, 128) and lse.shape == (0, 4)
+    none = torch.zeros(0, 2, 16, 128, dtype=torch.bfloat16, device=DEV)
+    adamas.chunk_attend(q, none, none, i32([0]), i32([]), ws)
+    kept, lens = adamas.evict(none, none, torch.zeros(0, 2, 16, device=DEV), i32([]), 4, ws)
+    assert kept.shape == (0, 2, 4) and lens.shape == (0,)
+    assert ws.device_error() == 0
+
+
+def test_captured_append_and_eviction():
+    """A captured decode-side run -- append, weights of kept tokens, eviction in place --
+    replayed on fresh copies of its caches gives the eager run's bits; two replays in a
+    row start from the same inputs again."""
+    B, Hq, Hkv, N, budget, keep = 2, 8, 2, 500, 32, 256
+    lens = [499, 380]
+    g = torch.Generator().manual_seed(71)
+    K0, V0 = make_cache(71, B, Hkv, N, [N, N], 0), make_cache(72, B, Hkv, N, [N, N], 0)
+    q, k, v = (torch.randn(B, h, 128, generator=g).to(torch.bfloat16).to(DEV) for h in (Hq, Hkv, Hkv))
+    idx = torch.stack([torch.stack([torch.randperm(n, generator=g)[:budget] for _ in range(Hq)]) for n in lens]).to(torch.int32).to(DEV)
+    m0 = torch.rand(B, Hkv, N, generator=g).to(DEV)
+    freqs, _ = adamas.rope_frequencies()
+    one, before, after = i32([0, 1, 2]), i32(lens), i32([n + 1 for n in lens])
+    ws = adamas.ChunkWorkspace(B, B, Hq, Hkv)
+    K, V, mass = torch.empty_like(K0), torch.empty_like(V0), torch.empty_like(m0)
+    codes = torch.zeros(K.shape[:-1] + (32,), dtype=torch.uint8, device=DEV)
+
+    def run():
+        K.copy_(K0), V.copy_(V0), mass.copy_(m0), codes.zero_()
+        r = adamas.rope_append(q, k, v, one, before, K, V, freqs, ws, codes=codes)
+        adamas.accumulate_kept(r, K, idx, after, mass, ws)
+        return (r, *adamas.evict(K, V, mass, after, keep, ws, codes=codes, n_sink=2, n_recent=8), K, V, mass, codes)
+
+    eager = [x.clone() for x in run()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = run()
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(eager, got))
+    assert ws.device_error() == 0
