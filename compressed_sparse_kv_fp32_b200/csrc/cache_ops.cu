@@ -152,7 +152,7 @@ static int rows_map(const void* base, int64_t rows, int box, CUtensorMap* map) {
   return tile_map(base, 2, dims, strides, boxes, map);
 }
 
-// The queries [T][Hq][128] for copies of 64 columns, G heads and TQ tokens.
+// The queries (or the outputs) [T][Hq][128] for copies of 64 columns, G heads and TQ tokens.
 static int query_map(const void* q, int T, int Hq, int G, int TQ, CUtensorMap* map) {
   const cuuint64_t dims[3] = {(cuuint64_t)kDim, (cuuint64_t)Hq, (cuuint64_t)T};
   const cuuint64_t strides[2] = {2 * kDim, (cuuint64_t)Hq * 2 * kDim};
@@ -299,8 +299,10 @@ int adamas_chunk_attend(const adamas_chunk_args* args, adamas_stream_t stream) {
   ap.TQ = 128 / p.G;
   const int64_t rows = cache_rows(a, p.geo);
   if (rows > INT32_MAX) return ADAMAS_ERR_UNSUPPORTED;
-  CUtensorMap q_map = {}, k_map = {}, v_map = {};
+  CUtensorMap q_map = {}, k_map = {}, v_map = {}, o_map = {};
   if ((rc = query_map(a.q, a.T, a.Hq, p.G, ap.TQ, &q_map)) != ADAMAS_OK) return rc;
+  ap.out_copies = 32 % p.G == 0;
+  if (ap.out_copies && (rc = query_map(a.out, a.T, a.Hq, p.G, 32 / p.G, &o_map)) != ADAMAS_OK) return rc;
   ap.box = rows > 0 ? rows_box(p.geo, a.page_size) : 0;
   if (ap.box && ((rc = rows_map(a.K, rows, ap.box, &k_map)) != ADAMAS_OK ||
                  (rc = rows_map(a.V, rows, ap.box, &v_map)) != ADAMAS_OK))
@@ -309,7 +311,7 @@ int adamas_chunk_attend(const adamas_chunk_args* args, adamas_stream_t stream) {
   const int64_t units = (int64_t)p.Hkv * ((a.T + 2 * ap.TQ - 1) / (2 * ap.TQ) + p.B);
   const int64_t tiles = units * ((p.geo.Nmax + 127) / 128 + 1);
   chunk_attend_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kAtThreads, kAtSmem, (cudaStream_t)stream>>>(
-      ap, q_map, k_map, v_map);
+      ap, q_map, k_map, v_map, o_map);
   return launched();
 }
 

@@ -6,9 +6,8 @@
 // K and V tile of 128 tokens.  Per tile: S = Q K^T (fp32, tensor memory), one running
 // maximum and sum per row, P = exp2(s c - m) rounded to bf16 in tensor memory over S,
 // O += P V (fp32, tensor memory).  The maximum that scales a row is raised only when a
-// score exceeds it by more than 2^8 in the exponent, so O is hardly ever rescaled; the
-// quotient is the same for every choice of it, and P and the sum stay far from fp32's
-// and bf16's range.
+// score exceeds it by more than kAtRaise, so O is hardly ever rescaled; the quotient is
+// the same for every choice of it.
 //
 // K and V tiles arrive by tensor-map copies of `box` rows -- all 128, or the largest
 // power of two of at least 8 rows that divides the page size -- one lane per page piece;
@@ -38,13 +37,23 @@ namespace adamas {
 
 constexpr int kAtThreads = 512;
 constexpr int kAtStages = 2;  // of K, and of V
+// A row's P is at most 2^32 and its sum and outputs at most 2^32 x 2^31 times a value: far
+// inside the range of bf16 and fp32, whose precision does not depend on the scale; what
+// underflows is 2^-94 of the largest and less.  (2^8: 1033 against 1012 us, 2048 new
+// tokens over 32K.)
+constexpr float kAtRaise = 32.0f;
 constexpr int kAtMaxGrid = 160;
 constexpr int kAtPartRow = 132;             // m, l, -, -, o[128]
 constexpr int64_t kAtL2Bytes = 48ll << 20;  // K and V of heads that go through a wave together
 
 // Where a block's share of the line begins, and how it goes on from there.
+struct AtSeq {  // a sequence of the batch: its rows and length
+  int first, n, len;
+};
 struct AtWalk {
   long long x, x1;  // [x, x1) of the line is still to do
+  AtSeq sq;         // the sequence at x
+  int hg;           // heads of its groups
   int b, group, q, h;  // sequence, group of heads, unit of the chunk, head in the group: the unit at x
   int t;               // x's place in the unit
 };
@@ -54,15 +63,19 @@ struct AtWalk {
 struct AtPlan {
   long long W;  // length of the line
   int shares;
+  int cost;     // places of a unit's start
   AtWalk start;
 };
-constexpr int kAtUnitCost = 1;  // a unit's start and end cost about as much as one K/V tile
+// A unit's start and end cost about as much as two K/V tiles; where a block has fewer than
+// four tiles, finer shares matter more and it counts as one (four sequences of one token
+// over 1000: 18 us, with two 23; prompts of up to 4096 tokens: 475 us, with two 411).
+constexpr int kAtUnitCost = 2, kAtCostTiles = 4;
 
 // 32 rows of 128 bytes per softmax warp: rows pass through on their way out, so that a
 // store covers whole lines
 constexpr int kAtRowsOut = 32 * 128;
 constexpr size_t kAtSmem = 2 * kTileBytes + 2 * kAtStages * kTileBytes + 8 * kAtRowsOut + 1024;
-static_assert((kMaxBatch + 1) * sizeof(long long) <= 2 * kTileBytes, "the plan's table lies over the first tiles");
+static_assert((kMaxBatch + 1) * sizeof(longlong2) <= 2 * kTileBytes, "the plan's table lies over the first tiles");
 
 struct AtParams {
   ChunkParams c;
@@ -71,6 +84,7 @@ struct AtParams {
   int part_rows;
   int TQ;             // tokens of one 128-row tile
   int box;            // rows of a tensor-map copy; 0: rows are copied one by one
+  int out_copies;     // a warp's 32 rows are whole tokens: they may leave by one copy
 };
 
 struct AtUnit {
@@ -89,11 +103,6 @@ struct AtSegment {
   int slot, ca, cb;  // partial state's place; blocks that share the unit
 };
 
-// A sequence of the batch: its rows and length.  (Read again for each unit: few lines, in
-// the first-level cache.)
-struct AtSeq {
-  int first, n, len;
-};
 __device__ __forceinline__ AtSeq at_seq(const AtParams& p, int b, bool& bad_cu, bool& bad_len) {
   AtSeq s;
   ragged_rows(p.c.cu_q, b, p.c.T, s.first, s.n, bad_cu);
@@ -129,22 +138,26 @@ __device__ __forceinline__ int at_group(const AtParams& p, const AtSeq& sq) {
   return fit < 1 ? 1 : (fit > (uint32_t)p.c.Hkv ? p.c.Hkv : (int)fit);
 }
 
+// a / b of two numbers that are nearly always below 2^32 (the long division takes 400 cycles).
+__device__ __forceinline__ long long at_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // The next piece of the block's share.  The line's order: sequences, groups of heads,
 // units from the chunk's last tokens to its first, heads of the group; a unit takes
-// kAtUnitCost places and one per K/V tile.
+// pl.cost places and one per K/V tile.
 __device__ __forceinline__ bool at_next(const AtPlan& pl, const AtParams& p, AtWalk& w, AtSegment& s) {
   while (w.x < w.x1) {
-    const AtSeq sq = at_seq(p, w.b);
-    const int hg = at_group(p, sq);
-    s.u = at_unit(p, sq, w.b, w.group * hg + w.h, w.q);
-    const long long f0 = w.x - w.t, f1 = f0 + kAtUnitCost + s.u.tiles, e = w.x1 < f1 ? w.x1 : f1;
-    s.t0 = w.t > kAtUnitCost ? w.t - kAtUnitCost : 0;
-    s.t1 = (int)(e - f0) - kAtUnitCost;
+    const int hg = w.hg;
+    s.u = at_unit(p, w.sq, w.b, w.group * hg + w.h, w.q);
+    const long long f0 = w.x - w.t, f1 = f0 + pl.cost + s.u.tiles, e = w.x1 < f1 ? w.x1 : f1;
+    s.t0 = w.t > pl.cost ? w.t - pl.cost : 0;
+    s.t1 = (int)(e - f0) - pl.cost;
     s.part = s.t0 != 0 || e != f1;
     s.slot = 2 * (int)blockIdx.x + (s.t0 == 0 ? 1 : 0);
     if (s.part) {  // the blocks whose shares hold the unit's first and last tile
-      s.ca = (int)(((f0 + kAtUnitCost + 1) * pl.shares - 1) / pl.W);
-      s.cb = (int)((f1 * pl.shares - 1) / pl.W);
+      s.ca = (int)at_div((f0 + pl.cost + 1) * pl.shares - 1, pl.W);
+      s.cb = (int)at_div(f1 * pl.shares - 1, pl.W);
     }
     w.x = e;
     w.t = 0;
@@ -152,13 +165,13 @@ __device__ __forceinline__ bool at_next(const AtPlan& pl, const AtParams& p, AtW
       w.h = 0;
       if (--w.q < 0) {
         ++w.group;
-        AtSeq nx = sq;
         if (w.group * hg >= p.c.Hkv) {
           w.group = 0;
-          do nx = at_seq(p, ++w.b);  // the line goes on, so a sequence with rows follows
-          while (nx.n == 0);
+          do w.sq = at_seq(p, ++w.b);  // the line goes on, so a sequence with rows follows
+          while (w.sq.n == 0);
+          w.hg = at_group(p, w.sq);
         }
-        w.q = at_units(p, nx) - 1;
+        w.q = at_units(p, w.sq) - 1;
       }
     }
     if (s.t1 > s.t0) return true;  // else the share ends before the unit's first tile
@@ -166,8 +179,8 @@ __device__ __forceinline__ bool at_next(const AtPlan& pl, const AtParams& p, AtW
   return false;
 }
 
-// tab: kMaxBatch + 1 numbers of shared memory, free again afterwards.
-__device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, long long* tab, int tid) {
+// tab: shared memory for kMaxBatch + 1 numbers, free again afterwards.
+__device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, longlong2* tab, int tid) {
   const int B = p.c.B, lane = tid & 31, warp = tid >> 5;
   for (int b = warp; b < B; b += kAtThreads / 32) {
     bool bad_cu = false, bad_len = false;
@@ -176,53 +189,60 @@ __device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, long
     if (lane == 0 && bad_len) atomicOr(p.c.err, kErrSeqLen);
     const int nu = at_units(p, sq);
     long long sum = 0;
-    for (int q = lane; q < nu; q += 32) sum += at_unit(p, sq, b, 0, q).tiles + kAtUnitCost;
+    for (int q = lane; q < nu; q += 32) sum += at_unit(p, sq, b, 0, q).tiles;
     if (nu > 1) {
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     }
-    if (lane == 0) tab[b + 1] = sum * p.c.Hkv;
+    if (lane == 0) tab[b + 1] = make_longlong2(sum * p.c.Hkv, (long long)nu * p.c.Hkv);  // tiles, units
   }
   __syncthreads();
   if (warp == 0) {
     long long all = 0;
+    for (int b = lane; b < B; b += 32) all += tab[b + 1].x;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+    const int cost = all >= (long long)kAtCostTiles * gridDim.x ? kAtUnitCost : 1;
+    all = 0;
     for (int b0 = 0; b0 < B; b0 += 32) {
-      long long s = b0 + lane < B ? tab[b0 + lane + 1] : 0;
+      long long s = 0;
+      if (b0 + lane < B) s = tab[b0 + lane + 1].x + cost * tab[b0 + lane + 1].y;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const long long u = __shfl_up_sync(0xffffffffu, s, d);
         if (lane >= d) s += u;
       }
       s += all;
-      if (b0 + lane < B) tab[b0 + lane + 1] = s;
+      if (b0 + lane < B) tab[b0 + lane + 1].x = s;  // from here on: places before the next sequence
       all = __shfl_sync(0xffffffffu, s, 31);
     }
-    if (lane == 0) tab[0] = 0;
+    if (lane == 0) tab[0].x = 0;
     __syncwarp();
     // a share is a unit's start and a tile at least
-    const long long most = all / (kAtUnitCost + 1);
+    const long long most = at_div(all, cost + 1);
     const int shares = most < (long long)gridDim.x ? (int)most : (int)gridDim.x;
-    AtWalk w = {0, 0, 0, 0, 0, 0, 0};
+    AtWalk w = {};
     if ((int)blockIdx.x < shares) {
-      const bool narrow = all < (1ll << 31) / kAtMaxGrid;
-      w.x = narrow ? (uint32_t)all * blockIdx.x / (uint32_t)shares : all * blockIdx.x / shares;
-      w.x1 = narrow ? (uint32_t)all * (blockIdx.x + 1) / (uint32_t)shares : all * (blockIdx.x + 1) / shares;
+      w.x = at_div(all * blockIdx.x, shares);
+      w.x1 = at_div(all * (blockIdx.x + 1), shares);
       int lo = 0, hi = B;  // tab[lo] <= x < tab[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (tab[mid] <= w.x) lo = mid;
+        if (tab[mid].x <= w.x) lo = mid;
         else hi = mid;
       }
       w.b = lo;
       const AtSeq sq = at_seq(p, lo);
       const int hg = at_group(p, sq), nu = at_units(p, sq);
-      const long long per_head = (tab[lo + 1] - tab[lo]) / p.c.Hkv, y0 = w.x - tab[lo];
-      w.group = (int)(y0 / (per_head * hg));
+      w.sq = sq;
+      w.hg = hg;
+      const long long per_head = at_div(tab[lo + 1].x - tab[lo].x, p.c.Hkv), y0 = w.x - tab[lo].x;
+      w.group = (int)at_div(y0, per_head * hg);
       long long y = y0 - w.group * hg * per_head, before = 0;
       const int hc = p.c.Hkv - w.group * hg < hg ? p.c.Hkv - w.group * hg : hg;
       for (int k0 = 0; k0 < nu; k0 += 32) {
-        const int cost = k0 + lane < nu ? at_unit(p, sq, lo, 0, nu - 1 - k0 - lane).tiles + kAtUnitCost : 0;
-        long long s = cost;
+        const int places = k0 + lane < nu ? at_unit(p, sq, lo, 0, nu - 1 - k0 - lane).tiles + cost : 0;
+        long long s = places;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const long long u = __shfl_up_sync(0xffffffffu, s, d);
@@ -231,10 +251,10 @@ __device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, long
         const uint32_t here = __ballot_sync(0xffffffffu, y < hc * (before + s));
         if (here) {
           const int l = __ffs(here) - 1;
-          const int cl = __shfl_sync(0xffffffffu, cost, l);
+          const int cl = __shfl_sync(0xffffffffu, places, l);
           y -= hc * (before + __shfl_sync(0xffffffffu, s, l) - cl);
           w.q = nu - 1 - k0 - l;
-          w.h = (int)(y / cl);
+          w.h = (int)at_div(y, cl);
           w.t = (int)(y - (long long)w.h * cl);
           break;
         }
@@ -244,6 +264,7 @@ __device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, long
     if (lane == 0) {
       pl.W = all;
       pl.shares = shares;
+      pl.cost = cost;
       pl.start = w;
     }
     fence_async_smem();  // tensor-map copies write over the table next
@@ -253,12 +274,15 @@ __device__ __forceinline__ void at_make_plan(AtPlan& pl, const AtParams& p, long
 
 // 32 rows of 128 bytes, one per lane in x, to their places (null: none): through shared
 // memory, so that each store instruction covers four whole lines.
-__device__ __forceinline__ void at_store_rows(uint32_t buf, const uint32_t (&x)[32], void* row, int lane) {
+__device__ __forceinline__ void at_stage_rows(uint32_t buf, const uint32_t (&x)[32], int lane) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
+  for (int c = 0; c < 8; ++c)  // in the 128-byte swizzle
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((c ^ (lane & 7)) << 4)), "r"(x[4 * c]),
                  "r"(x[4 * c + 1]), "r"(x[4 * c + 2]), "r"(x[4 * c + 3])
                  : "memory");
+}
+__device__ __forceinline__ void at_store_rows(uint32_t buf, const uint32_t (&x)[32], void* row, int lane) {
+  at_stage_rows(buf, x, lane);
   __syncwarp();
   const uint64_t mine = reinterpret_cast<uint64_t>(row);
 #pragma unroll
@@ -273,7 +297,7 @@ __device__ __forceinline__ void at_store_rows(uint32_t buf, const uint32_t (&x)[
 
 __global__ void __launch_bounds__(kAtThreads, 1)
     chunk_attend_kernel(const AtParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                        const __grid_constant__ CUtensorMap v_map) {
+                        const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap o_map) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ AtPlan pl;
   __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], k_full[kAtStages],
@@ -306,7 +330,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   }
   if (warp == 12) tmem_alloc512(&tmem_slot);
   tmem_fence_before();
-  at_make_plan(pl, p, reinterpret_cast<long long*>(smem_raw + (base - smem_addr(smem_raw))), tid);  // ends with a barrier
+  at_make_plan(pl, p, reinterpret_cast<longlong2*>(smem_raw + (base - smem_addr(smem_raw))), tid);  // ends with a barrier
   tmem_fence_after();
   const uint32_t tmem = tmem_slot;  // columns: S0 | S1 | O0 | O1, 128 each
 
@@ -357,7 +381,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               for (int k = 0; k < 4; ++k)
                 mx[k] = max3(mx[k], __uint_as_float(x[i >> 5][(i & 31) + k]), __uint_as_float(x[i >> 5][(i & 31) + 4 + k]));
             const float mt = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * kScoreLog2;
-            const bool raise = mt > m + 8.0f;  // also when m is -inf and a score is not
+            const bool raise = mt > m + kAtRaise;  // also when m is -inf and a score is not
             if (__any_sync(0xffffffffu, raise)) {
               const float mn = raise ? mt : m;
               const float f = raise ? fast_exp2(m - mn) : 1.0f;  // 0 when m was -inf
@@ -438,6 +462,36 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             fb *= inv;
           }
           const uint32_t buf = rows_out + warp * kAtRowsOut;
+          const bool whole = p.out_copies && __all_sync(0xffffffffu, live);
+          if (whole && !merge && !sg.part) {  // the common end of a prompt's unit, in as little code as it takes
+            if (lane == 0) tma_store_wait_read();
+            __syncwarp();
+            const uint64_t f2 = f2_pack(fa, fa);
+#pragma unroll 1
+            for (int c0 = 0; c0 < 128; c0 += 64) {
+              uint32_t x[32], z[32], y[32];
+              tmem_ld32(O + c0, x);
+              tmem_ld32(O + c0 + 32, z);
+              tmem_wait_ld(x);
+              tmem_wait_ld(z);
+              const uint64_t zero = 0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                float a, b;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(i < 16 ? x[2 * i] : z[2 * i - 32]),
+                                         __uint_as_float(i < 16 ? x[2 * i + 1] : z[2 * i - 31])), f2, zero), a, b);
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[i]) : "f"(b), "f"(a));
+              }
+              if (c0) {
+                if (lane == 0) tma_store_wait_read();
+                __syncwarp();
+              }
+              at_stage_rows(buf, y, lane);
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) tma_store_3d(&o_map, c0, sg.u.h * G, sg.u.row0 + tok, buf);
+            }
+          } else
 #pragma unroll 1
           for (int c0 = 0; c0 < 128; c0 += 64) {
             uint32_t y[32];
@@ -459,6 +513,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fa);
               }
               if (sg.part) {
+                if (lane == 0) tma_store_wait_read();
+                __syncwarp();
                 at_store_rows(buf, x, live ? st + 4 + c : nullptr, lane);
               } else {
 #pragma unroll
@@ -468,7 +524,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                       : "f"(__uint_as_float(x[2 * i + 1])), "f"(__uint_as_float(x[2 * i])));
               }
             }
-            if (!sg.part) at_store_rows(buf, y, live ? p.c.out + row * kDim + c0 : nullptr, lane);
+            if (!sg.part) {
+              if (lane == 0) tma_store_wait_read();
+              __syncwarp();
+              at_store_rows(buf, y, live ? p.c.out + row * kDim + c0 : nullptr, lane);
+            }
           }
           if (live) {
             if (sg.part) *reinterpret_cast<float2*>(st) = make_float2(m, l);
@@ -539,6 +599,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         named_sync(1, 256);  // last_flag is read before the next unit sets it
       }
     }
+    if (lane == 0) tma_store_wait();
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp < 12) {

@@ -188,6 +188,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
       : "memory");
 }
+// A box of a three-dimensional map from shared memory; the copies of a thread are committed
+// in groups, and it may wait until the last ones have read the memory, or are done.
+__device__ __forceinline__ void tma_store_3d(const void* map, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+               "r"(y), "r"(z), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // The barrier is arrived at once when every cp.async this thread issued before has landed
 // (the arrival counts as one of those the barrier expects).  Whoever waits for it runs
 // fence_async_smem() before the tensor core reads what landed.
