@@ -7,7 +7,9 @@ there is no fallback of any kind.
 
 Method: ADAMAS long-context sparse attention article (lnwmold.com/news/826806),
 §2.1 Hadamard rotation, §2.2 dynamic 2-bit bucketing, §3.1 packed code cache,
-§2.3 Manhattan-distance scoring, §5.2 token budget.
+§2.3 Manhattan-distance scoring, §5.2 token budget.  The cache operators at the end
+(rope_append, chunk_attend, accumulate_kept, accumulate_chunk, evict) are what a
+serving loop runs around the decode step on the same cache.
 """
 from __future__ import annotations
 

@@ -26,6 +26,16 @@
 // merges them in the blocks' order.  Sequences with several units (prompts) come first,
 // heads whose K and V fit in L2 together next to each other, so that the blocks at work
 // on them at one time read K and V from L2.
+// Products of one thread run in the order they were issued, which lets a tile's next S be
+// made over its P; a barrier's answer and a commit are what costs between them.
+//
+// Bound by reading K and V for few rows (8 sequences of 16K-32K, one token each, 32 over 8
+// heads: 145 us, 6.0 TB/s, 0.92 of the copy rate), and for many by the chain of one row
+// tile -- softmax 1900 cycles, its two products 1024, handing over some 700 -- two of
+// which share the tensor cores (2048 new tokens over 32K: 1.01 ms, 1050 TFLOP/s, 0.64 of
+// the matrix rate; 0.53 under the power cap of a long run).  Tried: an issuing thread per
+// row tile (the tiles fall into step: 1313 against 1087 us), halves of 64 tokens (1035
+// against 980), a share of the exponentials as polynomials (none faster).
 #pragma once
 
 #include <cuda.h>
@@ -37,11 +47,11 @@ namespace adamas {
 
 constexpr int kAtThreads = 512;
 constexpr int kAtStages = 2;  // of K, and of V
-// A row's P is at most 2^32 and its sum and outputs at most 2^32 x 2^31 times a value: far
+// A row's P is at most 2^16 and its sum and outputs at most 2^16 x 2^31 times a value: far
 // inside the range of bf16 and fp32, whose precision does not depend on the scale; what
-// underflows is 2^-94 of the largest and less.  (2^8: 1033 against 1012 us, 2048 new
+// underflows is 2^-110 of the largest and less.  (2^8: 1033 against 1012 us, 2048 new
 // tokens over 32K.)
-constexpr float kAtRaise = 32.0f;
+constexpr float kAtRaise = 16.0f;
 constexpr int kAtMaxGrid = 160;
 constexpr int kAtPartRow = 132;             // m, l, -, -, o[128]
 constexpr int64_t kAtL2Bytes = 48ll << 20;  // K and V of heads that go through a wave together

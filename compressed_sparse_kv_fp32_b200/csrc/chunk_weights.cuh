@@ -18,8 +18,9 @@
 // warps 16-17 copy K and Q tiles (and each column's -lse log2 e); one thread of warp 18
 // issues the products of even units, one of warp 19 those of odd ones.
 //
-// Bound by the exponentials (16 per cycle and multiprocessor) or, for short chunks, by
-// reading K.
+// Bound by the exponentials (16 per cycle and multiprocessor) and the latency around
+// them; for shorter chunks by reading K.  Measured: 64 rows of 32 heads (8 kv heads) over
+// 16K-32K tokens, batch 8, 148 us (the exponentials alone 75 us, the bytes 68 us).
 #pragma once
 
 #include "chunk_attend.cuh"

@@ -25,7 +25,8 @@ struct KeptParams {
 // to mass list after list, a barrier of the cluster between two lists, so that the weights
 // of two heads that kept the same token are added in a fixed order.  A list the query
 // heads share is read once, and its tokens get the heads' weights in one addition.
-// Bound by latency, then by the K rows.
+// Bound by latency, then by the K rows.  Measured: 32 heads of 1024 kept tokens of 128K
+// 7.7 us (8.8 MB; one block a head and the scores made three times: 34 us).
 constexpr int kKeptThreads = 256;
 constexpr int kKeptCluster = 8;
 constexpr int kKeptSmemFloats = 49152;
@@ -225,7 +226,8 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 // warp counts what it keeps of its run of tokens, and writes the kept slots in ascending
 // order behind those of the warps and blocks before it.  Bound by latency: up to five
 // exchanges between blocks.  (Digits of 11 bits, one exchange less, took twice as long:
-// the counts of eight blocks are then 64 KB a block and exchange.)
+// the counts of eight blocks are then 64 KB a block and exchange.)  Measured with the move:
+// 16 heads of 700 tokens 10.6 us, 32 heads from 32K to 1024 tokens 25 us.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBlockTokens = 2048;  // a block more for so many tokens, up to 8
@@ -427,7 +429,8 @@ __device__ __forceinline__ void move_group(MoveGroup& m, const EvictParams& p, i
 
 // To another cache: any block may move any rows.  A warp has kMoveGroups groups of rows on
 // their way at a time, and looks up where the next ones are meanwhile.  Bound by HBM
-// (2 x 548 bytes a token).
+// (2 x 548 bytes a token).  Measured: 4 x 8 heads of up to 32K tokens to 16K, pages to
+// pages, 148 us with the selection (580 MB: 3.9 TB/s, 0.60 of the copy rate).
 constexpr int kMoveThreads = 256;
 constexpr int kMoveGroups = 2;
 

@@ -136,7 +136,10 @@ __device__ __forceinline__ uint32_t encode128_half(uint4 raw, int l) {
 // query heads, the Hkv keys and the Hkv values in turn, two at a time) are on their way,
 // two warps per token find its sequence and place and evaluate its cos and sin; a row's
 // registers are asked for again as soon as it is done.  Bound by instructions and HBM
-// when there are many tokens, by latency for a few.
+// when there are many tokens, by latency for a few.  Measured: 12,506 tokens of 32 + 2 x 8
+// heads with codes 79 us (3.9 TB/s, 0.60 of the copy rate), one token of 32 + 2 x 32 heads
+// 3.6 us.  (One row a warp, every lane asking which half it holds: 229 us; cos and signed
+// sin kept per lane: 115; two rows a warp on packed pairs and two warps a token: 79.)
 constexpr int kRopeAhead = 4;  // pairs of rows
 constexpr int kRopeTokens = kRopeThreads / 64;
 
