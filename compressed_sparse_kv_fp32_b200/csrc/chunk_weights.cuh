@@ -20,7 +20,7 @@
 //
 // Bound by the exponentials (16 per cycle and multiprocessor) and the latency around
 // them; for shorter chunks by reading K.  Measured: 64 rows of 32 heads (8 kv heads) over
-// 16K-32K tokens, batch 8, 148 us (the exponentials alone 75 us, the bytes 68 us).
+// 16K-32K tokens, batch 8, 144 us (the exponentials alone 75 us, the bytes 68 us).
 #pragma once
 
 #include "chunk_attend.cuh"
@@ -35,6 +35,16 @@ struct WtParams {
   ChunkParams c;
   int TQ, box;
 };
+
+// What a block's time goes to when the chunk's rows stay, in places of about 400 cycles: a
+// unit takes kWtCostUnit and one for every 32 columns, but not less than reading its K; the
+// change to another head, at which everything on its way ends first, kWtCostHead.
+// (Measured a block: 2300 + 450 per 32 columns a unit, 7200 a change.  With a place for K
+// and one per Q tile the slowest block took 14% longer than the mean one: 158 us where this
+// takes 144, at the sizes above.)
+constexpr int kWtCostRead = 8;
+constexpr int kWtCostUnit = 6;
+constexpr int kWtCostHead = 18;
 
 struct WtUnit {
   int b, h, T0;      // sequence, kv head, first token
@@ -93,8 +103,8 @@ struct WtWalk {
     fills[0] = fills[1] = 0;
     if (u <= last) w = wt_unit(p, tab, u);
   }
-  // The first unit that begins at or behind place x when a sequence's units take
-  // (cost[b + 1] - cost[b]) / (tab[b + 1] - tab[b]) places each.
+  // The first unit that begins at or behind place x when the places of sequence b are
+  // [cost[b], cost[b + 1]): for each head the change to it and its units.
   static __device__ __forceinline__ int first_unit(const WtParams& p, const int* tab, const long long* cost, long long x) {
     int lo = 0, hi = p.c.B;  // cost[lo] <= x < cost[hi], or x is the end
     while (hi - lo > 1) {
@@ -102,10 +112,11 @@ struct WtWalk {
       if (cost[mid] <= x) lo = mid;
       else hi = mid;
     }
-    const int nu = tab[lo + 1] - tab[lo];
-    if (nu == 0) return tab[lo];
-    const long long each = (cost[lo + 1] - cost[lo]) / nu;
-    return tab[lo] + (int)((x - cost[lo] + each - 1) / each);
+    const int groups = (tab[lo + 1] - tab[lo]) / p.c.Hkv;
+    if (groups == 0) return tab[lo];
+    const long long head = (cost[lo + 1] - cost[lo]) / p.c.Hkv, each = (head - kWtCostHead) / groups;
+    const long long h = (x - cost[lo]) / head, in = x - cost[lo] - h * head - kWtCostHead;
+    return tab[lo] + (int)h * groups + (in <= 0 ? 0 : (int)((in + each - 1) / each));
   }
   __device__ __forceinline__ bool stays(const WtUnit& x) const { return x.q1 <= 2; }
   // prepares the unit at hand; false: none left
@@ -133,7 +144,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     chunk_weights_kernel(const WtParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ int tab[kMaxBatch + 1];         // units before each sequence
-  __shared__ long long cost[kMaxBatch + 1];  // and what they cost: a place for K, one per Q tile
+  __shared__ long long cost[kMaxBatch + 1];  // and what they cost, in places
   __shared__ __align__(16) float neg_lse[kWtStages][128];
   __shared__ __align__(8) uint64_t k_full[kWtStages], k_empty[kWtStages], q_full[kWtStages], q_empty[kWtStages],
       s_full[2][2], s_empty[2][2], all_done;
@@ -175,7 +186,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         if (bad_cu) atomicOr(p.c.err, kErrOffsets);
         if (bad_len) atomicOr(p.c.err, kErrSeqLen);
         if (n > 0) s = (len + 255) / 256 * p.c.Hkv;
-        z = (long long)s * (1 + (n + p.TQ - 1) / p.TQ);
+        if (s > 0)
+          z = (long long)p.c.Hkv * kWtCostHead +
+              (long long)s * max(kWtCostRead, kWtCostUnit + (min(n, 2 * p.TQ) * p.c.G + 31) / 32);
         most = n > most ? n : most;
       }
 #pragma unroll
@@ -249,13 +262,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           // 32 columns at a time, the next ones on their way meanwhile
           uint32_t xa[32], xb[32];
           auto add = [&](uint32_t (&x)[32], int i0) {
-            if (i0 >= c1) return;
-            if (some || i0 + 32 > c1) {  // columns that do not see the slot: a score of -inf
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = i0 + i >= c0 && i0 + i < c1 ? x[i] : 0xFF800000u;
-            }
 #pragma unroll
             for (int hf = 0; hf < 32; hf += 16) {
+              if (i0 + hf >= c1) break;
+              if (some || i0 + hf + 16 > c1) {  // columns that do not see the slot: a score of -inf
+#pragma unroll
+                for (int i = hf; i < hf + 16; ++i) x[i] = i0 + i >= c0 && i0 + i < c1 ? x[i] : 0xFF800000u;
+              }
               uint4 z[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) z[i] = lds128(nl + 4 * (i0 + hf) + 16 * i);
