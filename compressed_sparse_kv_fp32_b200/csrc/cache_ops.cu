@@ -57,9 +57,11 @@ static int check_ctrl(const void* ws, size_t bytes, size_t need) {
 static uint32_t* err_word(void* ws) { return static_cast<uint32_t*>(ws) + 2; }
 
 // A launch in clusters of C blocks; `most` bytes of dynamic shared memory are allowed to
-// the kernel once per device.
+// the kernel once per device.  `early`: its blocks may come in before the launch in front of
+// it is done (the kernel waits for that itself).
 template <auto Kernel, typename... Args>
-static int launch_cluster(int grid, int C, int threads, size_t smem, size_t most, cudaStream_t st, Args... args) {
+static int launch_cluster(int grid, int C, int threads, size_t smem, size_t most, bool early, cudaStream_t st,
+                          Args... args) {
   cudaError_t e;
   if (most > 48 * 1024) {
     static std::atomic<uint64_t> known{0};  // a bit per device
@@ -77,13 +79,15 @@ static int launch_cluster(int grid, int C, int threads, size_t smem, size_t most
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = early ? 2 : 1;
   if ((e = cudaLaunchKernelEx(&cfg, Kernel, args...)) != cudaSuccess) {
     (void)cudaGetLastError();
     return cuda_fail(e);
@@ -379,7 +383,7 @@ int adamas_accumulate_kept(const adamas_kept_args* args, adamas_stream_t stream)
     return launched();
   }
   return launch_cluster<accumulate_kept_kernel>(heads * C, C, kKeptThreads, (size_t)cap * p.G * sizeof(float),
-                        kKeptSmemFloats * sizeof(float), (cudaStream_t)stream, p, cap);
+                        kKeptSmemFloats * sizeof(float), false, (cudaStream_t)stream, p, cap);
 }
 
 int adamas_evict(const adamas_evict_args* args, adamas_stream_t stream) {
@@ -435,21 +439,20 @@ int adamas_evict(const adamas_evict_args* args, adamas_stream_t stream) {
   C = C < 1 ? 1 : (C > kSelCluster ? kSelCluster : C);
   const int64_t slice = (p.geo.Nmax + C - 1) / C;
   const size_t keys = slice <= kSelSmemTokens ? (size_t)slice * sizeof(uint32_t) : 0;
-  if ((rc = launch_cluster<evict_select_kernel>(heads * C, C, kSelThreads, keys, kSelSmemTokens * sizeof(uint32_t), st,
-                           p)) != ADAMAS_OK)
+  if ((rc = launch_cluster<evict_select_kernel>(heads * C, C, kSelThreads, keys, kSelSmemTokens * sizeof(uint32_t),
+                                                false, st, p)) != ADAMAS_OK)
     return rc;
   if (in_place) {  // a cluster per head, up to about one block per multiprocessor in all
     C = 1;
     while (C < 8 && (int64_t)heads * 2 * C <= 148 && a.keep >= 64 * C) C *= 2;
-    return launch_cluster<evict_shift_kernel>(heads * C, C, kShiftThreads, 0, 0, st, p);
+    return launch_cluster<evict_shift_kernel>(heads * C, C, kShiftThreads, 0, 0, true, st, p);
   }
   // 64 rows a block and round
   int per_head = (a.keep + 63) / 64;
   const int most = kCopyBlocks / heads;
   if (per_head > most) per_head = most;
   if (per_head < 1) per_head = 1;
-  evict_copy_kernel<<<(unsigned)(heads * per_head), kMoveThreads, 0, st>>>(p, per_head);
-  return launched();
+  return launch_cluster<evict_copy_kernel>(heads * per_head, 1, kMoveThreads, 0, 0, true, st, p, per_head);
 }
 
 }  // extern "C"

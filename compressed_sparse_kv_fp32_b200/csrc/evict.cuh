@@ -227,7 +227,7 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 // order behind those of the warps and blocks before it.  Bound by latency: up to five
 // exchanges between blocks.  (Digits of 11 bits, one exchange less, took twice as long:
 // the counts of eight blocks are then 64 KB a block and exchange.)  Measured with the move:
-// 16 heads of 700 tokens 10.6 us, 32 heads from 32K to 1024 tokens 25 us.
+// 16 heads of 700 tokens 10.0 us, 32 heads from 32K to 1024 tokens 23 us.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBlockTokens = 2048;  // a block more for so many tokens, up to 8
@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hk = blockIdx.x / C, b = hk / p.Hkv;
+  grid_launch_dependents();  // the moving kernel's blocks come in while the last of these are at work
   bool badlen = false;
   const int len = (int)clamp_len(p.seq_lens[b], p.geo.Nmax, badlen);
   const int k = p.keep < len ? p.keep : len;
@@ -430,7 +431,7 @@ __device__ __forceinline__ void move_group(MoveGroup& m, const EvictParams& p, i
 // To another cache: any block may move any rows.  A warp has kMoveGroups groups of rows on
 // their way at a time, and looks up where the next ones are meanwhile.  Bound by HBM
 // (2 x 548 bytes a token).  Measured: 4 x 8 heads of up to 32K tokens to 16K, pages to
-// pages, 148 us with the selection (580 MB: 3.9 TB/s, 0.60 of the copy rate).
+// pages, 140 us with the selection (580 MB: 4.1 TB/s, 0.63 of the copy rate).
 constexpr int kMoveThreads = 256;
 constexpr int kMoveGroups = 2;
 
@@ -464,6 +465,10 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_copy_kernel(const Evict
     }
   };
   auto count = [&](int j) { return k - j < 4 ? (k - j < 0 ? 0 : k - j) : 4; };
+  float* mass_out = p.mass_out + (int64_t)hk * p.out.Nmax;
+  for (int64_t t = k + part * kMoveThreads + threadIdx.x; t < p.out.Nmax; t += (int64_t)blocks_per_head * kMoveThreads)
+    mass_out[t] = 0.0f;
+  grid_dependency_wait();  // kept is there
   int j0 = (part * kWarps + warp) * 4;
   look_up(j0);
   for (; j0 < k; j0 += kMoveGroups * step) {
@@ -479,9 +484,6 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_copy_kernel(const Evict
     for (int g = 0; g < kMoveGroups; ++g)
       move_group<false>(m[g], p, dst[g], count(j0 + g * step), j0 + g * step + lane, hk, lane);
   }
-  float* mass_out = p.mass_out + (int64_t)hk * p.out.Nmax;
-  for (int64_t t = k + part * kMoveThreads + threadIdx.x; t < p.out.Nmax; t += (int64_t)blocks_per_head * kMoveThreads)
-    mass_out[t] = 0.0f;
   if (bad) atomicOr(p.err, kErrTable);
 }
 
@@ -504,6 +506,7 @@ __global__ void __launch_bounds__(kShiftThreads) evict_shift_kernel(const EvictP
   const int k = p.keep < len ? p.keep : len;
   bad = false;
   const int32_t* kept = p.kept + (int64_t)hk * p.keep;
+  grid_dependency_wait();  // kept is there
   int lo = 0, hi = k;  // the first j whose slot is not j: kept[j] - j never falls
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
