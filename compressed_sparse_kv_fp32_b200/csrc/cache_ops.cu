@@ -17,7 +17,7 @@ int cuda_fail(cudaError_t e);  // adamas.cu: records the error, returns ADAMAS_E
 
 static_assert(kErrOffsets == ADAMAS_DEVERR_OFFSETS, "error bits of the header");
 
-constexpr int kCopyBlocks = 148 * 3;  // as many as are resident: each then streams
+constexpr int kCopyBlocks = 148 * kMoveBlocks;  // as many as are resident: each then streams
 constexpr int64_t kRopeSplitBlocks = 592;  // blocks up to which a token's rows are split: four per multiprocessor
 constexpr size_t kCtrlBytes = 256;  // control words at the start of every workspace
 
@@ -447,8 +447,7 @@ int adamas_evict(const adamas_evict_args* args, adamas_stream_t stream) {
     while (C < 8 && (int64_t)heads * 2 * C <= 148 && a.keep >= 64 * C) C *= 2;
     return launch_cluster<evict_shift_kernel>(heads * C, C, kShiftThreads, 0, 0, true, st, p);
   }
-  // 64 rows a block and round
-  int per_head = (a.keep + 63) / 64;
+  int per_head = (int)(((int64_t)a.keep + 31) / 32);  // a round of a block's warps at least
   const int most = kCopyBlocks / heads;
   if (per_head > most) per_head = most;
   if (per_head < 1) per_head = 1;

@@ -227,7 +227,7 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 // order behind those of the warps and blocks before it.  Bound by latency: up to five
 // exchanges between blocks.  (Digits of 11 bits, one exchange less, took twice as long:
 // the counts of eight blocks are then 64 KB a block and exchange.)  Measured with the move:
-// 16 heads of 700 tokens 10.0 us, 32 heads from 32K to 1024 tokens 23 us.
+// 16 heads of 700 tokens 9.0 us, 32 heads from 32K to 1024 tokens 21 us.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBlockTokens = 2048;  // a block more for so many tokens, up to 8
@@ -428,15 +428,17 @@ __device__ __forceinline__ void move_group(MoveGroup& m, const EvictParams& p, i
   }
 }
 
-// To another cache: any block may move any rows.  A warp has kMoveGroups groups of rows on
-// their way at a time, and looks up where the next ones are meanwhile.  Bound by HBM
-// (2 x 548 bytes a token).  Measured: 4 x 8 heads of up to 32K tokens to 16K, pages to
-// pages, 140 us with the selection (580 MB: 4.1 TB/s, 0.63 of the copy rate).
+// To another cache: any block may move any rows; each has a run of them.  A warp has one
+// group of rows on its way and looks up where the next one is meanwhile; 32 such warps fill
+// a multiprocessor (two groups at a time leave room for 24 and took 140 us where this takes
+// 119).  Bound by HBM (2 x 548 bytes a token) and the chain slot - page - row.  Measured:
+// 4 x 8 heads of up to 32K tokens to 16K, pages to pages, 119 us with the selection (580 MB:
+// 4.9 TB/s, 0.74 of the copy rate).
 constexpr int kMoveThreads = 256;
-constexpr int kMoveGroups = 2;
+constexpr int kMoveBlocks = 4;  // a multiprocessor
 
-__global__ void __launch_bounds__(kMoveThreads, 3) evict_copy_kernel(const EvictParams p, int blocks_per_head) {
-  constexpr int kWarps = kMoveThreads / 32;
+__global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) evict_copy_kernel(const EvictParams p, int blocks_per_head) {
+  constexpr int kStep = kMoveThreads / 32 * 4;  // rows of a round of the block
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hk = blockIdx.x / blocks_per_head, part = blockIdx.x - hk * blocks_per_head;
   const int b = hk / p.Hkv, h = hk - b * p.Hkv;
@@ -445,44 +447,39 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_copy_kernel(const Evict
   const int k = p.keep < len ? p.keep : len;
   bad = false;
   const int32_t* kept = p.kept + (int64_t)hk * p.keep;
-  const int step = blocks_per_head * kWarps * 4;  // rows of a round of all warps
-  int64_t from[kMoveGroups], to[kMoveGroups];
-  int slot[kMoveGroups];
-  auto look_up = [&](int j0) {
-#pragma unroll
-    for (int g = 0; g < kMoveGroups; ++g) {
-      const int j = j0 + g * step + lane;
-      from[g] = to[g] = -1;
-      slot[g] = 0;
-      if (lane < 4 && j < k) {
-        bool bad_to = false;
-        slot[g] = kept[j];
-        from[g] = p.geo.row(b, h, slot[g], bad);
-        to[g] = p.out.row(b, h, j, bad_to);
-        if (bad_to) to[g] = -1;  // nothing is written through a bad entry
-        bad |= bad_to;
-      }
-    }
-  };
-  auto count = [&](int j) { return k - j < 4 ? (k - j < 0 ? 0 : k - j) : 4; };
+  // the block's rows, whole groups but for the last
+  const int groups = (int)(((int64_t)k + 3) / 4);
+  int j = (int)((int64_t)groups * part / blocks_per_head) * 4 + warp * 4;
+  const int64_t last = (int64_t)groups * (part + 1) / blocks_per_head * 4;
+  const int end = last < k ? (int)last : k;
   float* mass_out = p.mass_out + (int64_t)hk * p.out.Nmax;
-  for (int64_t t = k + part * kMoveThreads + threadIdx.x; t < p.out.Nmax; t += (int64_t)blocks_per_head * kMoveThreads)
+  for (int64_t t = (int64_t)k + part * kMoveThreads + threadIdx.x; t < p.out.Nmax;
+       t += (int64_t)blocks_per_head * kMoveThreads)
     mass_out[t] = 0.0f;
   grid_dependency_wait();  // kept is there
-  int j0 = (part * kWarps + warp) * 4;
-  look_up(j0);
-  for (; j0 < k; j0 += kMoveGroups * step) {
-    MoveGroup m[kMoveGroups];
-    int64_t dst[kMoveGroups];
-#pragma unroll
-    for (int g = 0; g < kMoveGroups; ++g) {
-      move_group<true>(m[g], p, from[g], count(j0 + g * step), slot[g], hk, lane);
-      dst[g] = to[g];
+  int64_t from, to;
+  int slot;
+  auto look_up = [&](int64_t j0) {
+    from = to = -1;
+    slot = 0;
+    if (lane < 4 && j0 + lane < end) {
+      bool bad_to = false;
+      slot = kept[j0 + lane];
+      from = p.geo.row(b, h, slot, bad);
+      to = p.out.row(b, h, (int)j0 + lane, bad_to);
+      if (bad_to) to = -1;  // nothing is written through a bad entry
+      bad |= bad_to;
     }
-    look_up(j0 + kMoveGroups * step);
-#pragma unroll
-    for (int g = 0; g < kMoveGroups; ++g)
-      move_group<false>(m[g], p, dst[g], count(j0 + g * step), j0 + g * step + lane, hk, lane);
+  };
+  look_up(j);
+  for (; j < end; j += kStep) {
+    MoveGroup m;
+    const int cnt = end - j < 4 ? end - j : 4;
+    const int64_t dst = to;
+    move_group<true>(m, p, from, cnt, slot, hk, lane);
+    look_up((int64_t)j + kStep);
+    move_group<false>(m, p, dst, cnt, j + lane, hk, lane);
+    if (end - j <= kStep) break;
   }
   if (bad) atomicOr(p.err, kErrTable);
 }
