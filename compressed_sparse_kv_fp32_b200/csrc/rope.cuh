@@ -34,7 +34,7 @@ struct RopeParams {
   uint64_t neg0;  // -0 twice
 };
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   uint32_t r;
@@ -137,14 +137,16 @@ __device__ __forceinline__ uint32_t encode128_half(uint4 raw, int l) {
 // two warps per token find its sequence and place and evaluate its cos and sin; a row's
 // registers are asked for again as soon as it is done.  Bound by instructions and HBM
 // when there are many tokens, by latency for a few.  Measured: 12,506 tokens of 32 + 2 x 8
-// heads with codes 79 us (3.9 TB/s, 0.60 of the copy rate), one token of 32 + 2 x 32 heads
-// 3.6 us.  (One row a warp, every lane asking which half it holds: 229 us; cos and signed
-// sin kept per lane: 115; two rows a warp on packed pairs and two warps a token: 79.)
+// heads with codes 74 us (4.2 TB/s, 0.64 of the copy rate), one token of 32 + 2 x 32 heads
+// 3.4 us.  (One row a warp, every lane asking which half it holds: 229 us; cos and signed
+// sin kept per lane: 115; two rows a warp on packed pairs and two warps a token: 79;
+// seven blocks of 128 threads a multiprocessor, whose 72 registers a thread are enough, for
+// four of 256 that kept some in memory: 74.)
 constexpr int kRopeAhead = 4;  // pairs of rows
 constexpr int kRopeTokens = kRopeThreads / 64;
 
 template <int MODE>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_append_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 7) rope_append_kernel(const RopeParams p) {
   __shared__ float2 cs[kRopeTokens][kDim / 2];
   __shared__ int64_t row0_of[kRopeTokens];  // its row in the cache's first head; -1: in no sequence, -2: not stored
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 15, hi = lane >> 4, e0 = 8 * l;
