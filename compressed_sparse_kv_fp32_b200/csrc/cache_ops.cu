@@ -438,9 +438,9 @@ int adamas_evict(const adamas_evict_args* args, adamas_stream_t stream) {
   int C = (int)((p.geo.Nmax + kSelBlockTokens - 1) / kSelBlockTokens);
   C = C < 1 ? 1 : (C > kSelCluster ? kSelCluster : C);
   const int64_t slice = (p.geo.Nmax + C - 1) / C;
-  const size_t keys = slice <= kSelSmemTokens ? (size_t)slice * sizeof(uint32_t) : 0;
-  if ((rc = launch_cluster<evict_select_kernel>(heads * C, C, kSelThreads, keys, kSelSmemTokens * sizeof(uint32_t),
-                                                false, st, p)) != ADAMAS_OK)
+  p.smem_keys = slice <= kSelSmemTokens ? (int)slice : kSelSmemSome;
+  if ((rc = launch_cluster<evict_select_kernel>(heads * C, C, kSelThreads, (size_t)p.smem_keys * sizeof(uint32_t),
+                                                kSelSmemTokens * sizeof(uint32_t), false, st, p)) != ADAMAS_OK)
     return rc;
   if (in_place) {  // a cluster per head, up to about one block per multiprocessor in all
     C = 1;

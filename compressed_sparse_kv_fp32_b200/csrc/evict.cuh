@@ -205,6 +205,7 @@ struct EvictParams {
   uint16_t *K_out, *V_out;
   uint8_t* codes_out;
   float* mass_out;
+  int smem_keys;  // keys of a slice that the selection's launch has shared memory for
   CacheGeom geo, out;
   uint32_t* err;
 };
@@ -219,11 +220,11 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 
 // ---------------------------------------------------------------- which tokens stay
 // A cluster of blocks per (b, kv head), a slice of the tokens each.  The keys are read
-// once into shared memory (a slice that does not fit is read again).  The k-th largest key
-// is found by 8-bit digits, most significant first: the blocks count their keys under the
-// digits known so far, each adds up the cluster's counts, and one warp finds the digit;
-// the rest of the digits need not be known once all keys under them are kept.  Then every
-// warp counts what it keeps of its run of tokens, and writes the kept slots in ascending
+// once into shared memory (a slice that does not fit what the launch has is read again).
+// The k-th largest key is found by 8-bit digits, most significant first: the blocks count
+// their keys under the digits known so far, each adds up the cluster's counts, and one warp
+// finds the digit; the rest of the digits need not be known once all keys under them are
+// kept.  Then every warp counts what it keeps of its run of tokens, and writes the kept slots in ascending
 // order behind those of the warps and blocks before it.  Bound by latency: up to five
 // exchanges between blocks.  (Digits of 11 bits, one exchange less, took twice as long:
 // the counts of eight blocks are then 64 KB a block and exchange.)  Measured with the move:
@@ -232,7 +233,11 @@ constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBlockTokens = 2048;  // a block more for so many tokens, up to 8
 constexpr int kSelCluster = 8;
-constexpr int kSelSmemTokens = 40960;  // keys of a slice kept in shared memory
+// Keys of a slice kept in shared memory.  The launch goes by the capacity, which the lengths
+// may be far below: where a full slice would not fit, there is room for the keys of shorter
+// ones that costs no resident block (32 heads of 400,000 tokens to 1024: 190 us; with room
+// for the most, one block a multiprocessor, 480).
+constexpr int kSelSmemTokens = 40960, kSelSmemSome = 10240;
 constexpr int kSelBins = 256;
 constexpr int kSelCopies = 8;          // counters of a digit, by lane, as lanes often agree
 
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   const int64_t recent0 = (int64_t)len - p.n_recent;
   // the block's slice, in runs of whole warps' loads so that every warp has one run
   const int t0 = (int)((int64_t)rank * len / C), t1 = (int)((int64_t)(rank + 1) * len / C);
-  const bool in_smem = t1 - t0 <= kSelSmemTokens;
+  const bool in_smem = t1 - t0 <= p.smem_keys;
   auto global_key = [&](int t) { return t < p.n_sink || t >= recent0 ? 0xFFFFFFFFu : mass_key(mass[t]); };
   if (in_smem) {
     for (int t = t0 + tid; t < t1; t += kSelThreads) sm_key[t - t0] = global_key(t);
