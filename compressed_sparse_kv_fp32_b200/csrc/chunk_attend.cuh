@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   __shared__ AtPlan pl;
   __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], k_full[kAtStages],
-      k_empty[kAtStages], v_full[kAtStages], v_empty[kAtStages], v_tail, all_done;
+      k_empty[kAtStages], v_full[kAtStages], v_empty[kAtStages], v_tail[kAtStages], all_done;
   __shared__ float2 duo[128];  // state of the second half of a one-tile unit
   __shared__ uint32_t tmem_slot, gave_up, last_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -332,8 +332,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 64);
       mbar_init(&v_empty[i], 1);
+      mbar_init(&v_tail[i], 1);
     }
-    mbar_init(&v_tail, 1);
     mbar_init(&all_done, 1);
     gave_up = 0;
     fence_mbar_init();
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
       AtWalk w = pl.start;
       AtSegment sg;
-      uint32_t it = 0, nseg = 0, tails = 0;
+      uint32_t it = 0, nseg = 0, tails = 0;  // bit i: parity of the phase of v_tail[i] that comes next
       bool bad = false;
       while (at_next(pl, p, w, sg)) {
         if (!is_v && lt == 0) {  // Q: TQ tokens' heads of the group are TQ * G rows of a tile
@@ -647,7 +647,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if (lt < pieces) row = p.c.geo.row32(sg.u.b, sg.u.h, j * 128 + lt * p.box, bad);
             mbar_wait_or_give_up(&empty[stage], par, &gave_up);
             const bool zeros = is_v && seen < 128;
-            uint64_t* bar = zeros ? &v_tail : &full[stage];
+            // (a tail's barrier is the stage's own: it is armed again only once both warps have
+            // arrived at full[stage], behind their wait for the phase before)
+            uint64_t* bar = zeros ? &v_tail[stage] : &full[stage];
             if (lt == 0) mbar_arrive_expect_tx(bar, (uint32_t)(pieces * p.box * 2 * kDim));
             if (lt < 32) {
               __syncwarp();
@@ -658,7 +660,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
               }
             }
             if (zeros) {
-              mbar_wait_or_give_up(&v_tail, tails++ & 1, &gave_up);
+              mbar_wait_or_give_up(bar, (tails >> stage) & 1, &gave_up);
+              tails ^= 1u << stage;
               for (int r = (seen < 0 ? 0 : seen) + lr; r < 128; r += 4)
                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + tile_piece(r, lc)), "r"(0) : "memory");
               fence_async_smem();

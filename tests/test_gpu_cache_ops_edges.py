@@ -54,3 +54,25 @@ def test_evict_behind_a_wide_block_table(lens, in_place):
                 assert base.same(got, old[t[b][src // page], h, src % page])
             mass = (dm if in_place else dst["mass_out"])[b, h].cpu().numpy()
             assert np.array_equal(mass[j].view(np.uint32), m[b, h, src].view(np.uint32)) and not mass[len(j):].any()
+
+
+# ---------------------------------------------------------------- attention: tiles that end inside, one after the other
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("lens", [
+    [0],                                      # rows that see nothing: tiles without a single copied row
+    [0, 5, 0, 0, 130, 0, 64, 1],
+    [1, 127, 100],
+    [129, 0, 255, 256, 0, 7],
+])
+def test_many_units_that_end_inside_a_tile(lens, page):
+    """Every block goes through a dozen units whose V tiles all have rows to be zeroed, many
+    of them without a row to be copied."""
+    n = 500
+    base.test_chunk_attend_and_its_weights(8, 4, [1 + (i * 7) % 3 for i in range(n)], [lens[i % len(lens)] for i in range(n)], 256,
+                                           page, 0, 0)
+
+
+def test_units_without_tokens_between_longer_ones():
+    ns = [40, 200, 1, 70, 3] * 20
+    lens = [0, 150, 0, 30, 512] * 20
+    base.test_chunk_attend_and_its_weights(6, 2, ns, lens, 512, 16, 1, 2)
