@@ -691,6 +691,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       // the copies land before the block goes, also when somebody gave up waiting for them
       for (uint32_t k = 1; k <= kAtStages && k <= it; ++k)
         mbar_wait_timed(&full[(it - k) % kAtStages], ((it - k) / kAtStages) & 1, 1000000000ull);
+      if (is_v)  // (a stage without a tail so far: the phase before its first one counts as over)
+        for (int i = 0; i < kAtStages; ++i) mbar_wait_timed(&v_tail[i], ((tails >> i) & 1) ^ 1, 1000000000ull);
       if (!is_v && nseg > 0) mbar_wait_timed(&q_full, (nseg - 1) & 1, 1000000000ull);
       if (bad) atomicOr(p.c.err, kErrTable);
     } else if (warp == 12) {
