@@ -2,8 +2,10 @@
 
 Argument marshalling only: every step of the method runs in the library's CUDA
 kernels.  Tensors are torch CUDA tensors; calls are enqueued on the current torch
-stream.  The library must have been built (compressed_sparse_kv_fp32_b200.build);
-there is no fallback of any kind.
+stream, or on `stream`, to which the tensors that such a call makes then belong
+(another stream waits for it before it reads them, and is recorded on them before
+they are given up).  The library must have been built
+(compressed_sparse_kv_fp32_b200.build); there is no fallback of any kind.
 
 Method: ADAMAS long-context sparse attention article (lnwmold.com/news/826806),
 §2.1 Hadamard rotation, §2.2 dynamic 2-bit bucketing, §3.1 packed code cache,
@@ -183,6 +185,16 @@ def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _make(fill, shape: tuple, dtype: torch.dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A tensor that a call makes for its results, by torch.empty or torch.zeros, as of the
+    stream that the call goes to: on the current one its fill could land behind the
+    call's kernels, and so could work that still writes to memory given back there."""
+    if stream is None:
+        return fill(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return fill(shape, dtype=dtype, device=device)
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -221,8 +233,7 @@ class Workspace:
     def __init__(self, B: int, Hq: int, Hkv: int, Nmax: int, budget: int, device=None,
                  stream: Optional[torch.cuda.Stream] = None, sharded: bool = False):
         self.nbytes = (shard_workspace_bytes if sharded else workspace_bytes)(B, Hq, Hkv, Nmax, budget)
-        self.buffer = torch.empty(self.nbytes, dtype=torch.uint8,
-                                  device=device if device is not None else "cuda")
+        self.buffer = _make(torch.empty, (self.nbytes,), torch.uint8, device if device is not None else "cuda", stream)
         self.reset(stream)
 
     def reset(self, stream: Optional[torch.cuda.Stream] = None):
@@ -256,7 +267,7 @@ def encode_keys(K: torch.Tensor, codes: torch.Tensor, pos_begin: Optional[torch.
     return codes
 
 
-def _decode_args(q, codes, K, V, seq_lens, budget, out, idx):
+def _decode_args(q, codes, K, V, seq_lens, budget, out, idx, stream):
     _need(q, "q", torch.bfloat16)
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, 128]")
@@ -270,9 +281,9 @@ def _decode_args(q, codes, K, V, seq_lens, budget, out, idx):
     _need(codes, "codes", torch.uint8, (B, Hkv, Nmax, d // 4))
     _need(seq_lens, "seq_lens", torch.int32, (B,))
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=torch.float32, device=q.device)
+        out = _make(torch.empty, (B, Hq, d), torch.float32, q.device, stream)
     if idx is None:
-        idx = torch.empty((B, Hq, budget), dtype=torch.int32, device=q.device)
+        idx = _make(torch.empty, (B, Hq, budget), torch.int32, q.device, stream)
     _need(out, "out", torch.float32, (B, Hq, d))
     _need(idx, "idx", torch.int32, (B, Hq, budget))
     return B, Hq, Hkv, Nmax, d, out, idx
@@ -283,7 +294,7 @@ def decode_step(q: torch.Tensor, codes: torch.Tensor, K: torch.Tensor, V: torch.
                 out: Optional[torch.Tensor] = None, idx: Optional[torch.Tensor] = None,
                 stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """One decode step: returns (out [B,Hq,128] fp32, idx [B,Hq,budget] int32)."""
-    B, Hq, Hkv, Nmax, d, out, idx = _decode_args(q, codes, K, V, seq_lens, budget, out, idx)
+    B, Hq, Hkv, Nmax, d, out, idx = _decode_args(q, codes, K, V, seq_lens, budget, out, idx, stream)
     rc = load().adamas_decode_step(q.data_ptr(), codes.data_ptr(), K.data_ptr(), V.data_ptr(),
                                    seq_lens.data_ptr(), B, Hq, Hkv, Nmax, d, budget, out.data_ptr(),
                                    idx.data_ptr() if budget > 0 else None,
@@ -298,7 +309,7 @@ def decode_step_append(q: torch.Tensor, codes: torch.Tensor, K: torch.Tensor, V:
                        stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """encode_keys of the key at append_pos[b] (int32 [B]; out of [0, Nmax): none)
     followed by decode_step, in one launch; codes is updated in place."""
-    B, Hq, Hkv, Nmax, d, out, idx = _decode_args(q, codes, K, V, seq_lens, budget, out, idx)
+    B, Hq, Hkv, Nmax, d, out, idx = _decode_args(q, codes, K, V, seq_lens, budget, out, idx, stream)
     _need(append_pos, "append_pos", torch.int32, (B,))
     rc = load().adamas_decode_step_append(q.data_ptr(), codes.data_ptr(), K.data_ptr(), V.data_ptr(),
                                           seq_lens.data_ptr(), append_pos.data_ptr(), B, Hq, Hkv, Nmax, d,
@@ -317,7 +328,7 @@ def score(q: torch.Tensor, codes: torch.Tensor, seq_lens: torch.Tensor, Hkv: Opt
     _, Hkv, Nmax, _ = codes.shape
     _need(codes, "codes", torch.uint8, (B, Hkv, Nmax, d // 4))
     _need(seq_lens, "seq_lens", torch.int32, (B,))
-    dist = torch.empty((B, Hq, Nmax), dtype=torch.int16, device=q.device)
+    dist = _make(torch.empty, (B, Hq, Nmax), torch.int16, q.device, stream)
     _check(load().adamas_score(q.data_ptr(), codes.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, Nmax, d,
                                dist.data_ptr(), _stream(stream)), "adamas_score")
     return dist
@@ -365,9 +376,9 @@ def decode(q: torch.Tensor, codes: torch.Tensor, K: torch.Tensor, V: torch.Tenso
     _need(seq_lens, "seq_lens", torch.int32, (B,))
     rows = Hkv if policy == SELECT_GROUP_SHARED else Hq
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=torch.float32, device=q.device)
+        out = _make(torch.empty, (B, Hq, d), torch.float32, q.device, stream)
     if idx is None:
-        idx = torch.empty((B, rows, budget), dtype=torch.int32, device=q.device)
+        idx = _make(torch.empty, (B, rows, budget), torch.int32, q.device, stream)
     _need(out, "out", torch.float32, (B, Hq, d))
     _need(idx, "idx", torch.int32, (B, rows, budget))
     if append_pos is not None:
@@ -409,7 +420,7 @@ def shard_score(q: torch.Tensor, codes: torch.Tensor, seq_lens: torch.Tensor, bu
     B, Hq, Hkv, Nmax, d = _shard_shapes(q, codes, seq_lens)
     _need(codes, "codes", torch.uint8, (B, Hkv, Nmax, d // 4))
     if hist is None:
-        hist = torch.empty((B, Hq, HIST_STRIDE), dtype=torch.int32, device=q.device)
+        hist = _make(torch.empty, (B, Hq, HIST_STRIDE), torch.int32, q.device, stream)
     _need(hist, "hist", torch.int32, (B, Hq, HIST_STRIDE))
     _check(load().adamas_shard_score(q.data_ptr(), codes.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, Nmax, d,
                                      budget, hist.data_ptr(), workspace.buffer.data_ptr(), workspace.nbytes,
@@ -432,9 +443,9 @@ def shard_attend(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens: to
     world = hist_all.shape[0]
     _need(hist_all, "hist_all", torch.int32, (world, B, Hq, HIST_STRIDE))
     if partial is None:
-        partial = torch.empty((B, Hq, PARTIAL_FLOATS), dtype=torch.float32, device=q.device)
+        partial = _make(torch.empty, (B, Hq, PARTIAL_FLOATS), torch.float32, q.device, stream)
     if idx is None:
-        idx = torch.empty((B, Hq, budget), dtype=torch.int32, device=q.device)
+        idx = _make(torch.empty, (B, Hq, budget), torch.int32, q.device, stream)
     _need(partial, "partial", torch.float32, (B, Hq, PARTIAL_FLOATS))
     _need(idx, "idx", torch.int32, (B, Hq, budget))
     _check(load().adamas_shard_attend(q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv,
@@ -452,7 +463,7 @@ def merge_partials(partials: torch.Tensor, out: Optional[torch.Tensor] = None,
     n, B, Hq, _ = partials.shape
     _need(partials, "partials", torch.float32, (n, B, Hq, PARTIAL_FLOATS))
     if out is None:
-        out = torch.empty((B, Hq, HEAD_DIM), dtype=torch.float32, device=partials.device)
+        out = _make(torch.empty, (B, Hq, HEAD_DIM), torch.float32, partials.device, stream)
     _need(out, "out", torch.float32, (B, Hq, HEAD_DIM))
     _check(load().adamas_merge_partials(partials.data_ptr(), n, B, Hq, out.data_ptr(), _stream(stream)),
            "adamas_merge_partials")
@@ -473,7 +484,7 @@ class ChunkWorkspace(Workspace):
 
     def __init__(self, T: int, B: int, Hq: int, Hkv: int, device=None, stream: Optional[torch.cuda.Stream] = None):
         self.nbytes = chunk_workspace_bytes(T, B, Hq, Hkv)
-        self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device if device is not None else "cuda")
+        self.buffer = _make(torch.empty, (self.nbytes,), torch.uint8, device if device is not None else "cuda", stream)
         self.reset(stream)
 
 
@@ -631,7 +642,7 @@ def rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optiona
         if out is not None:
             raise ValueError("out without q")
     elif out is None:
-        out = torch.zeros((T, Hq, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
+        out = _make(torch.zeros, (T, Hq, HEAD_DIM), torch.bfloat16, q.device, stream)
     a = RopeArgs(pq, pk, pv, sq, sk, sv, _on(dev, cu_new, "cu_new", torch.int32, (B + 1,)),
                  _on(dev, cache_lens, "cache_lens", torch.int32, (B,)),
                  _on(dev, positions, "positions", torch.int32, (T,)),
@@ -670,9 +681,9 @@ def chunk_attend(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.
     head, paged = _chunk_args(dev, q, K, V, cu_q, seq_lens, block_table)
     T, Hq = head[5], head[7]
     if out is None:
-        out = torch.zeros((T, Hq, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
+        out = _make(torch.zeros, (T, Hq, HEAD_DIM), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.zeros((T, Hq), dtype=torch.float32, device=q.device)
+        lse = _make(torch.zeros, (T, Hq), torch.float32, q.device, stream)
     a = ChunkArgs(*head, _on(dev, out, "out", torch.bfloat16, (T, Hq, HEAD_DIM)),
                   _on(dev, lse, "lse", torch.float32, (T, Hq)), None, *paged, workspace.buffer.data_ptr(),
                   workspace.nbytes)
@@ -750,9 +761,9 @@ def evict(K: torch.Tensor, V: torch.Tensor, mass: torch.Tensor, seq_lens: torch.
         if Hkv_out != Hkv:
             raise ValueError(f"K_out must have {Hkv} kv heads, got {Hkv_out}")
     if kept is None:
-        kept = torch.empty((B, Hkv, max(keep, 0)), dtype=torch.int32, device=K.device)
+        kept = _make(torch.empty, (B, Hkv, max(keep, 0)), torch.int32, K.device, stream)
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=K.device)
+        new_lens = _make(torch.empty, (B,), torch.int32, K.device, stream)
     a = EvictArgs(*ptrs, _on(dev, mass, "mass", torch.float32, (B, Hkv, Nmax)),
                   _on(dev, seq_lens, "seq_lens", torch.int32, (B,)), B, Hkv, Nmax, HEAD_DIM, keep, n_sink, n_recent,
                   _on(dev, kept, "kept", torch.int32, (B, Hkv, max(keep, 0))),

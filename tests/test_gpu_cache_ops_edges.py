@@ -76,3 +76,53 @@ def test_units_without_tokens_between_longer_ones():
     ns = [40, 200, 1, 70, 3] * 20
     lens = [0, 150, 0, 30, 512] * 20
     base.test_chunk_attend_and_its_weights(6, 2, ns, lens, 512, 16, 1, 2)
+
+
+# ---------------------------------------------------------------- results of a call on a stream of its own
+def calls():
+    """name -> (call of a stream, giving the tensors it made)."""
+    B, Hq, Hkv, N, keep = 2, 8, 2, 300, 40
+    g = torch.Generator().manual_seed(91)
+    q = torch.randn(21, Hq, 128, generator=g).to(torch.bfloat16).to(DEV)
+    k = torch.randn(21, Hkv, 128, generator=g).to(torch.bfloat16).to(DEV)
+    K, V = base.make_cache(92, B, Hkv, N, [N, N], 0), base.make_cache(93, B, Hkv, N, [N, N], 0)
+    codes = adamas.encode_keys(K, torch.zeros(B, Hkv, N, 32, dtype=torch.uint8, device=DEV))
+    mass = torch.rand(B, Hkv, N, generator=g).to(DEV)
+    cu, lens, none = base.i32([0, 20, 21]), base.i32([N, 211]), base.i32([0, 0])
+    freqs, _ = adamas.rope_frequencies()
+    to = dict(K_out=K[:, :, :keep].clone(), V_out=V[:, :, :keep].clone(), mass_out=mass[:, :, :keep].clone())
+    ws, dws, sws = adamas.ChunkWorkspace(21, B, Hq, Hkv), adamas.Workspace(B, Hq, Hkv, N, 32), adamas.Workspace(B, Hq, Hkv, N, 32, sharded=True)
+    K2, V2, q1 = K.clone(), V.clone(), q[:2].contiguous()
+    hist = adamas.shard_score(q1, codes, lens, 32, sws).unsqueeze(0)
+    partial = adamas.shard_attend(q1, K, V, lens, 32, hist, 0, sws)[0].unsqueeze(0)
+    return {
+        "rope_append": lambda s: (adamas.rope_append(q, k, k, cu, none, K2, V2, freqs, ws, stream=s),),
+        "chunk_attend": lambda s: adamas.chunk_attend(q, K, V, cu, lens, ws, stream=s),
+        "evict": lambda s: adamas.evict(K, V, mass, lens, keep, ws, stream=s, **to),
+        "decode": lambda s: adamas.decode(q1, codes, K, V, lens, 32, dws, stream=s),
+        "decode_step": lambda s: adamas.decode_step(q1, codes, K, V, lens, 32, dws, stream=s),
+        "score": lambda s: (adamas.score(q1, codes, lens, stream=s),),
+        "shard_score": lambda s: (adamas.shard_score(q1, codes, lens, 32, sws, stream=s),),
+        "shard_attend": lambda s: (adamas.shard_score(q1, codes, lens, 32, sws, stream=s), *adamas.shard_attend(q1, K, V, lens, 32, hist, 0, sws, stream=s)),
+        "merge_partials": lambda s: (adamas.merge_partials(partial, stream=s),),
+        "workspace": lambda s: (adamas.ChunkWorkspace(21, B, Hq, Hkv, stream=s).buffer, adamas.Workspace(B, Hq, Hkv, N, 32, stream=s).buffer),
+    }
+
+
+@pytest.mark.parametrize("name", ["rope_append", "chunk_attend", "evict", "decode", "decode_step", "score", "shard_score",
+                                  "shard_attend", "merge_partials", "workspace"])
+def test_results_belong_to_the_stream_of_the_call(name):
+    """What a call makes for its results must not wait for the current stream: neither is it
+    filled there behind the call, nor is it memory that work queued there still writes to."""
+    call = calls()[name]
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    blocks = [torch.empty_like(t) for t in want for _ in range(8)]
+    torch.cuda._sleep(200000000)                     # a tenth of a second of the current stream
+    for x in blocks:
+        x.view(torch.uint8).fill_(0x55)
+    del blocks, x                                    # given back: to the current stream's next tensors
+    got = call(side)
+    torch.cuda.synchronize()
+    assert all(base.same(a, b) for a, b in zip(got, want, strict=True))
