@@ -522,7 +522,7 @@ def rope_frequencies(rot_dim: int = HEAD_DIM, base: float = 10000.0, *, scaling:
         def pair_of(turns):  # the pair that turns this often within original_len
             return rot_dim * math.log(original_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
         lo = max(0, math.floor(pair_of(beta_fast)))
-        hi = min(half - 1, math.ceil(pair_of(beta_slow)))
+        hi = min(rot_dim - 1, math.ceil(pair_of(beta_slow)))  # may lie behind the last pair: none is that slow
         ramp = [min(1.0, max(0.0, (j - lo) / max(hi - lo, 1e-3))) for j in range(half)]
         freq = [f * (1.0 - r) + f / factor * r for f, r in zip(freq, ramp)]
         mscale = 0.1 * math.log(factor) + 1.0
