@@ -169,6 +169,15 @@ __global__ void __launch_bounds__(kRopeThreads, 7) rope_append_kernel(const Rope
 #pragma unroll
   for (int j = 0; j < kRopeAhead; ++j) raw[j] = ask(i0 + j * stride);
 
+  if (blockIdx.x == 0 && blockIdx.y == 0) {  // the offsets of sequences that no row is looked up in, too
+    bool bad = false;
+#pragma unroll 1
+    for (int b = threadIdx.x; b < p.B; b += kRopeThreads) {
+      int first, n;
+      ragged_rows(p.cu_new, b, p.T, first, n, bad);
+    }
+    if (bad) atomicOr(p.err, kErrOffsets);
+  }
   if (part < 2 && r < p.T) {
     int below = 0;  // the sequence of row r is the last one that starts at or before it
     for (int b0 = 0; b0 < p.B; b0 += 32)
@@ -176,9 +185,8 @@ __global__ void __launch_bounds__(kRopeThreads, 7) rope_append_kernel(const Rope
     int64_t row0 = -1;
     if (below > 0) {
       int first, n;
-      bool bad = false;
+      bool bad = false;  // flagged above
       ragged_rows(p.cu_new, below - 1, p.T, first, n, bad);
-      if (bad && lane == 0) atomicOr(p.err, kErrOffsets);
       if (r >= first && r < first + n) {
         const int64_t slot = (int64_t)p.cache_lens[below - 1] + (r - first);
         const int pair = part * 32 + lane;

@@ -126,3 +126,31 @@ def test_results_belong_to_the_stream_of_the_call(name):
     got = call(side)
     torch.cuda.synchronize()
     assert all(base.same(a, b) for a, b in zip(got, want, strict=True))
+
+
+# ---------------------------------------------------------------- offsets that are no offsets
+@pytest.mark.parametrize("T,cu", [(3, [0, 4]), (3, [-1, 2]), (3, [2, 1]), (3, [5, 3]), (3, [0, 1, 0]), (3, [0, 0, 7, 7]),
+                                  (3, [2, 2, 1, 2]), (600, [600] * 200 + [599] + [600] * 300)])
+def test_bad_offsets_are_flagged_by_every_call(T, cu):
+    B = len(cu) - 1
+    q = torch.randn(T, 2, 128, generator=torch.Generator().manual_seed(95)).to(torch.bfloat16).to(DEV)
+    K = torch.zeros(B, 2, 8, 128, dtype=torch.bfloat16, device=DEV)
+    ws, lens = adamas.ChunkWorkspace(T, B, 2, 2), base.i32([8] * B)
+    lse, mass = torch.zeros(T, 2, device=DEV), torch.zeros(B, 2, 8, device=DEV)
+    freqs, _ = adamas.rope_frequencies()
+    for call in (lambda: adamas.rope_append(q, None, None, base.i32(cu), lens, K, K, freqs, ws),
+                 lambda: adamas.rope_append(None, q, q, base.i32(cu), lens, K, K, freqs, ws),
+                 lambda: adamas.chunk_attend(q, K, K, base.i32(cu), lens, ws),
+                 lambda: adamas.accumulate_chunk(q, K, lse, base.i32(cu), lens, mass, ws)):
+        call()
+        assert ws.device_error() == adamas.DEVERR_OFFSETS
+        ws.reset()
+
+
+def test_good_offsets_are_not_flagged():
+    q = torch.randn(4, 2, 128, generator=torch.Generator().manual_seed(96)).to(torch.bfloat16).to(DEV)
+    K = torch.zeros(3, 2, 8, 128, dtype=torch.bfloat16, device=DEV)
+    ws, freqs = adamas.ChunkWorkspace(4, 3, 2, 2), adamas.rope_frequencies()[0]
+    for cu in ([0, 0, 0, 0], [4, 4, 4, 4], [1, 2, 2, 3], [0, 4, 4, 4]):
+        adamas.rope_append(q, q, q, base.i32(cu), base.i32([1, 2, 3]), K, K.clone(), freqs, ws)
+        assert ws.device_error() == 0
