@@ -603,7 +603,7 @@ def _packed_rows(dev, x: Optional[torch.Tensor], name: str):
     row, head, one = x.stride()
     if T and (one != 1 or (H > 1 and head != d)):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return T, H, row if T > 1 else max(H * d, row // 8 * 8), x.data_ptr()
+    return T, H, row if T > 1 else H * d, x.data_ptr()  # one row has no spacing
 
 
 def rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],

@@ -154,3 +154,20 @@ def test_good_offsets_are_not_flagged():
     for cu in ([0, 0, 0, 0], [4, 4, 4, 4], [1, 2, 2, 3], [0, 4, 4, 4]):
         adamas.rope_append(q, q, q, base.i32(cu), base.i32([1, 2, 3]), K, K.clone(), freqs, ws)
         assert ws.device_error() == 0
+
+
+# ---------------------------------------------------------------- one token that is part of a projection's row
+@pytest.mark.parametrize("rot,inter", [(128, False), (128, True), (6, False)])
+def test_one_token_is_rotated_in_place_in_its_projection(rot, inter):
+    Hq, Hkv = 4, 2
+    row = torch.randn(1, Hq + 2 * Hkv, 128, generator=torch.Generator().manual_seed(97)).to(torch.bfloat16).to(DEV)
+    q, k, v = row.split([Hq, Hkv, Hkv], 1)
+    assert q.stride(0) == row.stride(0)
+    K, V = (torch.zeros(1, Hkv, 9, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    ws, freqs = adamas.ChunkWorkspace(1, 1, Hq, Hkv), adamas.rope_frequencies(rot)[0]
+    cu, before = base.i32([0, 1]), base.i32([5])
+    want = adamas.rope_append(q, k, v, cu, before, K, V, freqs, ws, interleaved=inter)
+    K2, V2, rest = torch.zeros_like(K), torch.zeros_like(V), row[:, Hq:].clone()
+    assert adamas.rope_append(q, k, v, cu, before, K2, V2, freqs, ws, interleaved=inter, out=q) is q
+    assert base.same(row[:, :Hq], want) and base.same(row[:, Hq:], rest)
+    assert base.same(K, K2) and base.same(V, V2) and ws.device_error() == 0
