@@ -561,6 +561,13 @@ def _device_of(t: torch.Tensor, name: str) -> int:
     return dev
 
 
+def _scratch(dev: int, workspace: Workspace) -> Tuple[int, int]:
+    """Address and size of a call's workspace, which must be on the call's device."""
+    if workspace.buffer.get_device() != dev:
+        raise ValueError(f"workspace must be on cuda:{dev}, got {workspace.buffer.device}")
+    return workspace.buffer.data_ptr(), workspace.nbytes
+
+
 def _run(name: str, args: ctypes.Structure, stream: Optional[torch.cuda.Stream]):
     rc = getattr(_lib if _lib is not None else load(), name)(ctypes.byref(args), _stream(stream))
     if rc != 0:
@@ -648,7 +655,7 @@ def rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optiona
                  _on(dev, positions, "positions", torch.int32, (T,)),
                  _on(dev, freqs, "freqs", torch.int64, freqs.shape), 2 * freqs.shape[0], int(interleaved), mscale,
                  T, B, Hq or Hkv, Hkv, Nmax, HEAD_DIM, _on(dev, out, "out", torch.bfloat16, (T, Hq, HEAD_DIM)),
-                 *ptrs, *paged, workspace.buffer.data_ptr(), workspace.nbytes)
+                 *ptrs, *paged, *_scratch(dev, workspace))
     _run("adamas_rope_append", a, stream)
     return out
 
@@ -685,8 +692,7 @@ def chunk_attend(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.
     if lse is None:
         lse = _make(torch.zeros, (T, Hq), torch.float32, q.device, stream)
     a = ChunkArgs(*head, _on(dev, out, "out", torch.bfloat16, (T, Hq, HEAD_DIM)),
-                  _on(dev, lse, "lse", torch.float32, (T, Hq)), None, *paged, workspace.buffer.data_ptr(),
-                  workspace.nbytes)
+                  _on(dev, lse, "lse", torch.float32, (T, Hq)), None, *paged, *_scratch(dev, workspace))
     _run("adamas_chunk_attend", a, stream)
     return out, lse
 
@@ -701,8 +707,7 @@ def accumulate_chunk(q: torch.Tensor, K: torch.Tensor, lse: torch.Tensor, cu_q: 
     head, paged = _chunk_args(dev, q, K, None, cu_q, seq_lens, block_table)
     T, B, Hq, Hkv, Nmax = head[5:10]
     a = ChunkArgs(*head, None, _on(dev, lse, "lse", torch.float32, (T, Hq)),
-                  _on(dev, mass, "mass", torch.float32, (B, Hkv, Nmax)), *paged, workspace.buffer.data_ptr(),
-                  workspace.nbytes)
+                  _on(dev, mass, "mass", torch.float32, (B, Hkv, Nmax)), *paged, *_scratch(dev, workspace))
     _run("adamas_accumulate_chunk", a, stream)
     return mass
 
@@ -726,8 +731,7 @@ def accumulate_kept(q: torch.Tensor, K: torch.Tensor, idx: torch.Tensor, seq_len
     a = KeptArgs(_on(dev, q, "q", torch.bfloat16, (B, Hq, HEAD_DIM)), pk,
                  _on(dev, idx, "idx", torch.int32, (B, rows, budget)),
                  _on(dev, seq_lens, "seq_lens", torch.int32, (B,)), B, Hq, Hkv, Nmax, HEAD_DIM, budget, policy,
-                 _on(dev, mass, "mass", torch.float32, (B, Hkv, Nmax)), *paged, workspace.buffer.data_ptr(),
-                 workspace.nbytes)
+                 _on(dev, mass, "mass", torch.float32, (B, Hkv, Nmax)), *paged, *_scratch(dev, workspace))
     _run("adamas_accumulate_kept", a, stream)
     return mass
 
@@ -769,6 +773,6 @@ def evict(K: torch.Tensor, V: torch.Tensor, mass: torch.Tensor, seq_lens: torch.
                   _on(dev, kept, "kept", torch.int32, (B, Hkv, max(keep, 0))),
                   _on(dev, new_lens, "new_lens", torch.int32, (B,)), *paged, *ptrs_out,
                   _on(dev, mass_out, "mass_out", torch.float32, (B, Hkv, Nmax_out)), Nmax_out, *paged_out,
-                  workspace.buffer.data_ptr(), workspace.nbytes)
+                  *_scratch(dev, workspace))
     _run("adamas_evict", a, stream)
     return kept, new_lens

@@ -171,3 +171,20 @@ def test_one_token_is_rotated_in_place_in_its_projection(rot, inter):
     assert adamas.rope_append(q, k, v, cu, before, K2, V2, freqs, ws, interleaved=inter, out=q) is q
     assert base.same(row[:, :Hq], want) and base.same(row[:, Hq:], rest)
     assert base.same(K, K2) and base.same(V, V2) and ws.device_error() == 0
+
+
+# ---------------------------------------------------------------- a workspace that is somewhere else
+def test_a_workspace_of_another_device_is_refused():
+    class Elsewhere:
+        buffer, nbytes = torch.zeros(1 << 20, dtype=torch.uint8), 1 << 20
+
+    q = torch.zeros(1, 2, 128, dtype=torch.bfloat16, device=DEV)
+    K = torch.zeros(1, 2, 8, 128, dtype=torch.bfloat16, device=DEV)
+    lens, cu, mass, ws = base.i32([8]), base.i32([0, 1]), torch.zeros(1, 2, 8, device=DEV), Elsewhere()
+    for call in (lambda: adamas.rope_append(q, q, q, cu, base.i32([0]), K, K, adamas.rope_frequencies()[0], ws),
+                 lambda: adamas.chunk_attend(q, K, K, cu, lens, ws),
+                 lambda: adamas.accumulate_chunk(q, K, torch.zeros(1, 2, device=DEV), cu, lens, mass, ws),
+                 lambda: adamas.accumulate_kept(q, K, torch.zeros(1, 2, 4, dtype=torch.int32, device=DEV), lens, mass, ws),
+                 lambda: adamas.evict(K, K.clone(), mass, lens, 4, ws)):
+        with pytest.raises(ValueError, match="workspace"):
+            call()
