@@ -17,7 +17,6 @@ struct ChunkParams {
   uint32_t* err;
 };
 
-constexpr float kScoreScale = 0.08838834764831845f;               // 1 / sqrt(128)
 constexpr float kScoreLog2 = 0.08838834764831845f * 1.4426950408889634f;  // ... log2 e
 
 }  // namespace adamas
