@@ -18,7 +18,7 @@ int cuda_fail(cudaError_t e);  // adamas.cu: records the error, returns ADAMAS_E
 static_assert(kErrOffsets == ADAMAS_DEVERR_OFFSETS, "error bits of the header");
 
 constexpr int kCopyBlocks = 148 * kMoveBlocks;  // as many as are resident: each then streams
-constexpr int64_t kRopeSplitBlocks = 592;  // blocks up to which a token's rows are split: four per multiprocessor
+constexpr int64_t kRopeSplitBlocks = 592;  // blocks up to which a token's rows are split: four a multiprocessor, of the seven that fit
 constexpr size_t kCtrlBytes = 256;  // control words at the start of every workspace
 
 static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }

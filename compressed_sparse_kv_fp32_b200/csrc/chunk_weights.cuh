@@ -6,7 +6,8 @@
 // heads of the group; for a short chunk from L2).  S^T = K Q^T (fp32, tensor memory) has
 // a token per row, so that a thread sums its own token's weights over the columns: no
 // exchange between threads, and the sums come in a fixed order.  Each token's total gets
-// one addition, by one thread.
+// one addition, by one thread.  The exponentials are ex2.approx, 2 ulp of fp32: the totals
+// are off by 1.8e-7 of their size, those of 32-bit exponentials summed in torch by 8e-8.
 //
 // A chunk of at most two Q tiles stays in shared memory over all units of its head that a
 // block does one after the other (its units are then neighbours); longer chunks stream

@@ -24,7 +24,8 @@ struct KeptParams {
 // stay in shared memory.  The blocks exchange maxima and sums; then the weights are added
 // to mass list after list, a barrier of the cluster between two lists, so that the weights
 // of two heads that kept the same token are added in a fixed order.  A list the query
-// heads share is read once, and its tokens get the heads' weights in one addition.
+// heads share is read once, and its tokens get the heads' weights in one addition.  The
+// exponentials are ex2.approx, 2 ulp of fp32.
 // Bound by latency, then by the K rows.  Measured: 32 heads of 1024 kept tokens of 128K
 // 7.7 us (8.8 MB; one block a head and the scores made three times: 34 us).
 constexpr int kKeptThreads = 256;
@@ -224,9 +225,10 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 // The k-th largest key is found by 8-bit digits, most significant first: the blocks count
 // their keys under the digits known so far, each adds up the cluster's counts, and one warp
 // finds the digit; the rest of the digits need not be known once all keys under them are
-// kept.  Then every warp counts what it keeps of its run of tokens, and writes the kept slots in ascending
-// order behind those of the warps and blocks before it.  Bound by latency: up to five
-// exchanges between blocks.  (Digits of 11 bits, one exchange less, took twice as long:
+// kept.  Then every warp counts what it keeps of its run of tokens, and writes the kept
+// slots in ascending order behind those of the warps and blocks before it.  Bound by
+// latency: up to five exchanges between blocks, or, for a block that is alone (up to 2048
+// tokens), its own barriers and the clearing of its counters.  (Digits of 11 bits, one exchange less, took twice as long:
 // the counts of eight blocks are then 64 KB a block and exchange.)  Measured with the move:
 // 16 heads of 700 tokens 9.0 us, 32 heads from 32K to 1024 tokens 21 us.
 constexpr int kSelThreads = 512;

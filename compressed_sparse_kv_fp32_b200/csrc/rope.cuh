@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kRopeThreads, 7) rope_append_kernel(const Rope
   __shared__ int64_t row0_of[kRopeTokens];  // its row in the cache's first head; -1: in no sequence, -2: not stored
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 15, hi = lane >> 4, e0 = 8 * l;
   const int nq = p.q ? p.Hq : 0, nk = p.k ? p.Hkv : 0, rows = nq + 2 * nk, pairs = (rows + 1) >> 1;
-  const int share = (kRopeThreads / 32) / p.tokens;  // warps of a token: 8 or 2
+  const int share = (kRopeThreads / 32) / p.tokens;  // warps of a token: 4 or 2
   const int tk = warp / share, part = warp - tk * share;
   const int64_t r = (int64_t)blockIdx.x * p.tokens + tk;
   const int stride = gridDim.y * share, i0 = r < p.T ? blockIdx.y * share + part : pairs;

@@ -188,3 +188,24 @@ def test_a_workspace_of_another_device_is_refused():
                  lambda: adamas.evict(K, K.clone(), mass, lens, 4, ws)):
         with pytest.raises(ValueError, match="workspace"):
             call()
+
+
+def test_a_captured_run_over_two_streams():
+    """Part of a captured run goes to a second stream that the first one forks to and joins;
+    its results are of the graph's memory like the others."""
+    call = calls()["chunk_attend"]
+    want = [t.clone() for t in call(None)]
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        got = call(side)
+        main.wait_stream(side)
+        twice = [t + t for t in got]
+    for _ in range(2):
+        for t in (*got, *twice):
+            t.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(base.same(a, b) and base.same(a + a, c) for a, b, c in zip(want, got, twice, strict=True))
